@@ -29,7 +29,9 @@ EXPORTS = ("attn_abi_version", "attn_status_string", "attn_last_error_detail", "
            "attn_decode_workspace_bytes", "attn_decode", "attn_decode_num_splits",
            "attn_get_device_error", "attn_debug_timeout_probe", "attn_decode_noalloc",
            "attn_fwd_varlen", "attn_decode_paged", "attn_bwd", "attn_bwd_workspace_bytes", "attn_fwd_fp8",
-           "attn_fwd_block_sparse")
+           "attn_fwd_block_sparse", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd",
+           "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_paged", "attn_page_update",
+           "attn_decode_shared_prefix", "attn_decode_shared_prefix_workspace_bytes")
 
 # size of the library-owned scratch array behind attn_decode_noalloc (include/attn.h)
 DECODE_NOALLOC_MAX_BYTES = 64 << 20
@@ -84,6 +86,20 @@ def lib():
         L.attn_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.attn_bwd.argtypes = [vp] * 9 + [i] * 9 + [f, vp, ctypes.c_size_t, vp]
         L.attn_bwd.restype = i
+        L.attn_qk_norm_rope.argtypes = [vp] * 10 + [i] * 10 + [f, vp]
+        L.attn_qk_norm_rope.restype = i
+        L.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i]
+        L.attn_qk_norm_rope_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.attn_qk_norm_rope_bwd.argtypes = [vp] * 14 + [i] * 10 + [f, vp, ctypes.c_size_t, vp]
+        L.attn_qk_norm_rope_bwd.restype = i
+        L.attn_qk_norm_rope_paged.argtypes = [vp] * 13 + [i] * 10 + [f, vp]
+        L.attn_qk_norm_rope_paged.restype = i
+        L.attn_page_update.argtypes = [vp] * 10 + [i] * 5 + [vp]
+        L.attn_page_update.restype = i
+        L.attn_decode_shared_prefix_workspace_bytes.argtypes = [i] * 7
+        L.attn_decode_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
+        L.attn_decode_shared_prefix.argtypes = [vp] * 10 + [i] * 11 + [f, vp, ctypes.c_size_t, vp]
+        L.attn_decode_shared_prefix.restype = i
         _lib = L
     return _lib
 
@@ -500,6 +516,328 @@ def attn_decode_noalloc(q, k, v, o=None, lse=None, scale=None, num_splits=0, ret
                                        Nk, d, scale, int(num_splits), _stream_ptr(stream))
     _raise(rc, "attn_decode_noalloc")
     return o, lse
+
+
+def attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len, max_seq_len,
+                                              d) -> int:
+    return int(lib().attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len,
+                                                               max_seq_len, d))
+
+
+def attn_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts,
+                              block_table, seq_lens, max_prefix_len, max_seq_len, o=None, lse=None,
+                              scale=None, workspace=None, return_lse=True, stream=None):
+    """Decode for sequences behind shared prefixes, over a paged cache.
+
+    q [B,Hq,1,d] bf16; k_cache/v_cache [num_pages,page_size,Hkv,d] bf16; prefix g has prefix_lens[g]
+    keys in pages prefix_table[g] ([num_groups,max_prefix_pages] int32) and is shared by sequences
+    group_starts[g] .. group_starts[g+1]-1 (int32 [num_groups+1], device); block_table
+    [B,max_pages_per_seq] and seq_lens [B] int32 hold each sequence's own keys.  max_prefix_len and
+    max_seq_len are ints >= every length.  Returns (o [B,Hq,1,d] bf16, lse [B,Hq] fp32).
+    """
+    import torch
+
+    B, Hq, d = _decode_query(q)
+    _check(k_cache, "k_cache", torch.bfloat16, 4)
+    num_pages, page_size, Hkv, dk = k_cache.shape
+    if dk != d:
+        raise ValueError("k_cache and v_cache must both be [num_pages, page_size, Hkv, d]")
+    _check(v_cache, "v_cache", torch.bfloat16, 4, k_cache.shape)
+    _check(prefix_table, "prefix_table", torch.int32, 2)
+    num_groups = prefix_table.shape[0]
+    _check(prefix_lens, "prefix_lens", torch.int32, 1, (num_groups,))
+    _check(group_starts, "group_starts", torch.int32, 1, (num_groups + 1,))
+    _check(block_table, "block_table", torch.int32, 2)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table and seq_lens need one row per sequence")
+    _check(seq_lens, "seq_lens", torch.int32, 1, (B,))
+    _check_out(o, "o", torch.bfloat16, (B, Hq, 1, d))
+    _check_out(lse, "lse", torch.float32, (B, Hq))
+    _check_workspace(workspace, 0)
+    dev = _device(stream, q=q, k_cache=k_cache, v_cache=v_cache, prefix_table=prefix_table,
+                  prefix_lens=prefix_lens, group_starts=group_starts, block_table=block_table,
+                  seq_lens=seq_lens, o=o, lse=lse, workspace=workspace)
+    max_prefix_len, max_seq_len = int(max_prefix_len), int(max_seq_len)
+    with torch.cuda.device(dev):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None and return_lse:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        if workspace is None:
+            nbytes = attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len,
+                                                               max_seq_len, d)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+        rc = lib().attn_decode_shared_prefix(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(prefix_table),
+            _ptr(prefix_lens), _ptr(group_starts), _ptr(block_table), _ptr(seq_lens), B, Hq, Hkv,
+            num_groups, num_pages, page_size, prefix_table.shape[1], max_prefix_len,
+            block_table.shape[1], max_seq_len, d, scale, _ptr(workspace), workspace.numel(),
+            _stream_ptr(stream))
+    _raise(rc, "attn_decode_shared_prefix")
+    return o, lse
+
+
+def _check_view(t, name, dtype, shape, written=False):
+    """A strided tensor argument: type, dtype, shape and a contiguous last dimension; one that is
+    written must not hold an element twice (an expanded or self-overlapping view)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if t.stride(-1) != 1:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
+    if written and not t.is_contiguous():
+        end = 1
+        for step, n in sorted((t.stride(i), t.shape[i]) for i in range(t.dim()) if t.shape[i] > 1):
+            if step < end:
+                raise ValueError("%s overlaps itself: a tensor that is written needs rows of its own" % name)
+            end = step * (n - 1) + end
+
+
+def _bhn(t):
+    """(b, h, n) element strides of a [B,H,N,d] or packed [T,H,d] tensor."""
+    s = t.stride()
+    return s[:3] if len(s) == 4 else (0, s[1], s[0])
+
+
+class _QkShapes:
+    """Shapes of a norm + rotation call, dense [B,H,N,d] or packed [T,H,d]: checks q, k, the weights,
+    the table, the positions and the sections, and keeps what the library is told about them."""
+
+    def __init__(self, q, k, q_weight, k_weight, rope, positions, sections):
+        import torch
+
+        if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor):
+            raise TypeError("q and k must be torch.Tensors")
+        if q.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("q must be torch.bfloat16 or torch.float32, got %s" % q.dtype)
+        if q.dim() not in (3, 4) or k.dim() != q.dim():
+            raise ValueError("q and k must both be [B, H, N, d] or both packed [tokens, H, d]")
+        self.dtype, self.code = q.dtype, 0 if q.dtype == torch.bfloat16 else 1
+        self.dense = q.dim() == 4
+        if self.dense:
+            self.B, self.Hq, self.N, self.d = q.shape
+            self.Hkv = k.shape[1]
+        else:
+            self.B, (self.N, self.Hq, self.d) = 1, q.shape
+            self.Hkv = k.shape[1]
+        self.q_shape, self.k_shape = self.shape(self.Hq), self.shape(self.Hkv)
+        _check_view(q, "q", self.dtype, self.q_shape)
+        _check_view(k, "k", self.dtype, self.k_shape)
+        for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if t is not None:
+                _check(t, n, self.dtype, 1, (self.d,))
+        _check(rope, "rope", torch.float32, 2)
+        self.max_pos, self.rot = rope.shape
+        self.sections, self.axes = None, 1
+        if sections is not None:
+            sections = [int(x) for x in sections]
+            self.axes = len(sections)
+            if not 1 <= self.axes <= 4 or min(sections) < 0 or 2 * sum(sections) != self.rot:
+                raise ValueError("sections must be 1 to 4 counts of pairs that add up to rope.shape[1] / 2 = %d, got %s"
+                                 % (self.rot // 2, sections))
+            self.sections = (ctypes.c_int * self.axes)(*sections)
+        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
+            raise TypeError("positions must be a torch.int32 tensor")
+        lead = () if sections is None else (self.axes,)
+        wants = [lead + (self.N,)] + ([lead + (self.B, self.N)] if self.dense else [])
+        if tuple(positions.shape) not in wants:
+            raise ValueError("positions must have shape %s, got %s"
+                             % (" or ".join(map(str, wants)), tuple(positions.shape)))
+        if self.N > 1 and positions.stride(-1) != 1:
+            raise ValueError("positions must be contiguous in its last dimension")
+        self.pos = (positions.stride(0) if lead else 0,
+                    positions.stride(-2) if positions.dim() == len(lead) + 2 else 0)
+
+    def shape(self, heads):
+        return (self.B, heads, self.N, self.d) if self.dense else (self.N, heads, self.d)
+
+
+def _longs(*parts):
+    flat = [x for p in parts for x in p]
+    return (ctypes.c_longlong * len(flat))(*flat)
+
+
+def attn_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, sections=None, interleaved=False,
+                      eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Queries and keys normalised per head, weighted and rotated by position, in one pass.
+
+    q [B,Hq,N,d], k [B,Hkv,N,d] (attn_fwd's layout) or packed q [T,Hq,d], k [T,Hkv,d]
+    (attn_fwd_varlen's), bf16 or fp32, d 64 or 128; any strides with d contiguous and 16-byte rows, as
+    views into a fused projection have.  q_weight, k_weight [d] in the same type, or None where that
+    side is not normalised.  rope fp32 [max_pos, rot_dim]: cosines, then sines, of each position's
+    angles; rot_dim a multiple of 16 up to d.  positions int32 [N] or [B,N] ([T] packed); with sections
+    (the rotated pairs of each position axis) [axes,N] or [axes,B,N] ([axes,T]).  interleaved pairs
+    columns (2i, 2i+1) instead of (i, i + rot_dim/2).
+
+    Returns (q_out, k_out), contiguous unless given; an output may be its input.
+    """
+    import torch
+
+    s = _QkShapes(q, k, q_weight, k_weight, rope, positions, sections)
+    if q_out is not None:
+        _check_view(q_out, "q_out", s.dtype, s.q_shape, written=True)
+    if k_out is not None:
+        _check_view(k_out, "k_out", s.dtype, s.k_shape, written=True)
+    dev = _device(stream, q=q, k=k, q_weight=q_weight, k_weight=k_weight, rope=rope,
+                  positions=positions, q_out=q_out, k_out=k_out)
+    with torch.cuda.device(dev):
+        if q_out is None:
+            q_out = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
+        if k_out is None:
+            k_out = torch.empty(s.k_shape, dtype=s.dtype, device=dev)
+        rc = lib().attn_qk_norm_rope(
+            _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(q_weight), _ptr(k_weight), _ptr(rope),
+            _ptr(positions), _longs(_bhn(q), _bhn(k), _bhn(q_out), _bhn(k_out), s.pos), s.sections,
+            s.code, s.B, s.N, s.Hq, s.Hkv, s.d, s.rot, s.max_pos, s.axes, int(interleaved),
+            float(eps), _stream_ptr(stream))
+    _raise(rc, "attn_qk_norm_rope")
+    return q_out, k_out
+
+
+def attn_qk_norm_rope_bwd_workspace_bytes(d) -> int:
+    return int(lib().attn_qk_norm_rope_bwd_workspace_bytes(d))
+
+
+def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, sections=None,
+                          interleaved=False, eps=1e-6, dq=None, dk=None, dq_weight=None,
+                          dk_weight=None, workspace=None, stream=None):
+    """Gradient of attn_qk_norm_rope: dq_out, dk_out are the gradients of its outputs (attn_bwd's dq
+    and dk), the other arguments those of the call.
+
+    Returns (dq, dk, dq_weight, dk_weight): dq, dk like q, k (contiguous unless given), the weights'
+    gradients fp32 [d], None where there is no weight.
+    """
+    import torch
+
+    s = _QkShapes(q, k, q_weight, k_weight, rope, positions, sections)
+    _check_view(dq_out, "dq_out", s.dtype, s.q_shape)
+    _check_view(dk_out, "dk_out", s.dtype, s.k_shape)
+    if dq is not None:
+        _check_view(dq, "dq", s.dtype, s.q_shape, written=True)
+    if dk is not None:
+        _check_view(dk, "dk", s.dtype, s.k_shape, written=True)
+    for t, w, n in ((dq_weight, q_weight, "dq_weight"), (dk_weight, k_weight, "dk_weight")):
+        if t is not None and w is None:
+            raise ValueError("%s is given but the weight is not" % n)
+        _check_out(t, n, torch.float32, (s.d,))
+    _check_workspace(workspace, 0)
+    dev = _device(stream, q=q, k=k, dq_out=dq_out, dk_out=dk_out, q_weight=q_weight, k_weight=k_weight,
+                  rope=rope, positions=positions, dq=dq, dk=dk, dq_weight=dq_weight,
+                  dk_weight=dk_weight, workspace=workspace)
+    with torch.cuda.device(dev):
+        if dq is None:
+            dq = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
+        if dk is None:
+            dk = torch.empty(s.k_shape, dtype=s.dtype, device=dev)
+        if dq_weight is None and q_weight is not None:
+            dq_weight = torch.empty(s.d, dtype=torch.float32, device=dev)
+        if dk_weight is None and k_weight is not None:
+            dk_weight = torch.empty(s.d, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(attn_qk_norm_rope_bwd_workspace_bytes(s.d), 16),
+                                    dtype=torch.uint8, device=dev)
+        rc = lib().attn_qk_norm_rope_bwd(
+            _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(q_weight),
+            _ptr(k_weight), _ptr(dq_weight), _ptr(dk_weight), _ptr(rope), _ptr(positions),
+            _longs(_bhn(q), _bhn(k), _bhn(dq_out), _bhn(dk_out), _bhn(dq), _bhn(dk), s.pos),
+            s.sections, s.code, s.B, s.N, s.Hq, s.Hkv, s.d, s.rot, s.max_pos, s.axes,
+            int(interleaved), float(eps), _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+    _raise(rc, "attn_qk_norm_rope_bwd")
+    return dq, dk, dq_weight, dk_weight
+
+
+def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, rope, positions, slots, k_cache, v_cache,
+                            sections=None, interleaved=False, eps=1e-6, q_out=None, stream=None):
+    """attn_qk_norm_rope for serving: q [T,Hq,d] goes to q_out, k (normalised, rotated) and v
+    [T,Hkv,d] into rows slots[t] of the paged cache k_cache / v_cache [num_pages,page_size,Hkv,d]
+    (bf16, d 128; q, k, v any strides with d contiguous and 16-byte rows).  slots int32 [T], distinct;
+    a token with a negative slot is left out.  Returns q_out [T,Hq,d], contiguous unless given: as
+    [T,Hq,1,d] (unsqueeze(2)) it is the decode calls' q.  Rows of left-out tokens keep what q_out held.
+    """
+    import torch
+
+    s = _QkShapes(q, k, q_weight, k_weight, rope, positions, sections)
+    if s.dense or s.dtype != torch.bfloat16:
+        raise ValueError("q, k and v must be packed bf16 [tokens, H, d] tensors")
+    _check_view(v, "v", s.dtype, s.k_shape)
+    _check(slots, "slots", torch.int32, 1, (s.N,))
+    _check(k_cache, "k_cache", torch.bfloat16, 4)
+    num_pages, page_size = k_cache.shape[:2]
+    _check(k_cache, "k_cache", torch.bfloat16, 4, (num_pages, page_size, s.Hkv, s.d))
+    _check(v_cache, "v_cache", torch.bfloat16, 4, k_cache.shape)
+    if q_out is not None:
+        _check_view(q_out, "q_out", s.dtype, s.q_shape, written=True)
+    dev = _device(stream, q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, rope=rope,
+                  positions=positions, slots=slots, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
+    with torch.cuda.device(dev):
+        if q_out is None:
+            q_out = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
+        rc = lib().attn_qk_norm_rope_paged(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(q_weight),
+            _ptr(k_weight), _ptr(rope), _ptr(positions), _ptr(slots),
+            _longs(_bhn(q), _bhn(k), _bhn(v), _bhn(q_out), s.pos[:1]), s.sections, s.N, s.Hq, s.Hkv,
+            num_pages, page_size, s.d, s.rot, s.max_pos, s.axes, int(interleaved), float(eps),
+            _stream_ptr(stream))
+    _raise(rc, "attn_qk_norm_rope_paged")
+    return q_out
+
+
+def attn_page_update(block_table, old_lens, new_lens, free_pages, ring, page_size, max_tokens,
+                     pos_offset=None, ring_out=None, cu_seqlens=None, slots=None, positions=None,
+                     stream=None):
+    """One step of a paged cache's bookkeeping, on the device: requests grow from old_lens to
+    new_lens (int32 [B]), shrink (rejected tokens, 0 for an ended request) or stay.
+
+    block_table int32 [B,max_pages_per_seq] and free_pages int32 [num_pages] (a ring of free page
+    numbers) are updated in place; ring int64 [3] holds the ring's head and tail (free entries are
+    head .. tail-1 modulo num_pages; a fresh pool is arange(num_pages) with [0, num_pages, 0]).
+
+    Returns (ring_out int64 [3], cu_seqlens int32 [B+1], slots int32 [max_tokens], positions int32
+    [max_tokens]): ring for the next step, with the number of pages missing in ring_out[2] (0: done;
+    > 0: the pool is short, -1: invalid lengths; nothing was changed then), the new tokens' offsets
+    per request, and each new token's cache row and position (plus pos_offset[b], int32 [B]); -1 and
+    0 behind the last.  ring_out must not be ring.
+    """
+    import torch
+
+    _check(block_table, "block_table", torch.int32, 2)
+    B, max_pages = block_table.shape
+    _check(old_lens, "old_lens", torch.int32, 1, (B,))
+    _check(new_lens, "new_lens", torch.int32, 1, (B,))
+    _check(free_pages, "free_pages", torch.int32, 1)
+    _check(ring, "ring", torch.int64, 1, (3,))
+    max_tokens = int(max_tokens)
+    if max_tokens < 0:
+        raise ValueError("max_tokens must not be negative")
+    _check_out(pos_offset, "pos_offset", torch.int32, (B,))
+    _check_out(ring_out, "ring_out", torch.int64, (3,))
+    _check_out(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    _check_out(slots, "slots", torch.int32, (max_tokens,))
+    _check_out(positions, "positions", torch.int32, (max_tokens,))
+    dev = _device(stream, block_table=block_table, old_lens=old_lens, new_lens=new_lens,
+                  free_pages=free_pages, ring=ring, pos_offset=pos_offset, ring_out=ring_out,
+                  cu_seqlens=cu_seqlens, slots=slots, positions=positions)
+    with torch.cuda.device(dev):
+        if ring_out is None:
+            ring_out = torch.empty(3, dtype=torch.int64, device=dev)
+        if cu_seqlens is None:
+            cu_seqlens = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        if slots is None:
+            slots = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+        if positions is None:
+            positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+        rc = lib().attn_page_update(
+            _ptr(block_table), _ptr(old_lens), _ptr(new_lens), _ptr(free_pages), _ptr(ring),
+            _ptr(ring_out), _ptr(cu_seqlens), _ptr(slots), _ptr(positions), _ptr(pos_offset), B,
+            max_pages, int(page_size), free_pages.numel(), max_tokens, _stream_ptr(stream))
+    _raise(rc, "attn_page_update")
+    return ring_out, cu_seqlens, slots, positions
 
 
 def attn_get_device_error(stream=None) -> int:

@@ -15,9 +15,12 @@
 #include "bwd_sm100.cuh"
 #include "common.cuh"
 #include "decode.cuh"
+#include "decode_prefix.cuh"
 #include "decode_tc.cuh"
 #include "fwd_f32.cuh"
 #include "fwd_sm100.cuh"
+#include "pages.cuh"
+#include "qk_norm_rope.cuh"
 
 namespace attn {
 namespace {
@@ -32,6 +35,8 @@ struct DeviceInfo {
   bool fwd_configured = false;
   bool bwd_configured = false;
   bool dtc_configured = false;
+  bool pfx_configured = false;
+  bool pages_configured = false;
 };
 
 std::mutex g_mutex;
@@ -1072,3 +1077,461 @@ extern "C" int attn_decode_noalloc(const void* q, const void* k, const void* v, 
   return attn_decode(q, k, v, o, lse, B, Hq, Hkv, Nk, d, scale, num_splits, scratch,
                      ATTN_DECODE_NOALLOC_MAX_BYTES, stream);
 }
+
+// ------------------------------------------------------------------------------------------
+// Around attention: queries and keys on their way to it, the paged cache's bookkeeping, and decode
+// behind shared prefixes.
+// ------------------------------------------------------------------------------------------
+namespace attn {
+namespace {
+
+// A [B][H][N][d] view: 16-byte rows for the vector loads (strides of single entries do not count).
+bool view_ok(const void* base, const long long* st, int B, int H, int N, int size) {
+  const long long mask = 16 / size - 1;
+  return aligned16(base) && (B <= 1 || (st[0] & mask) == 0) && (H <= 1 || (st[1] & mask) == 0) &&
+         (N <= 1 || (st[2] & mask) == 0);
+}
+
+qkn::View make_view(const long long* st) { return qkn::View{st[0], st[1], st[2]}; }
+
+// Argument rules shared by the norm + rotation calls; fills what they share of the parameters.
+int qkn_common(qkn::Params& p, const void* q_weight, const void* k_weight, const float* rope,
+               const int* positions, const int* sections, int dtype, int B, int N, int Hq, int Hkv,
+               int d, int rot_dim, int max_pos, int num_axes, float eps) {
+  if (B < 0 || N < 0 || Hq < 1 || Hkv < 1) return ATTN_ERR_INVALID_ARG;
+  if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_F32) return ATTN_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > d || rot_dim % 16 != 0 || max_pos < 0) return ATTN_ERR_INVALID_ARG;
+  if (num_axes < 1 || num_axes > qkn::kMaxAxes) return ATTN_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  const bool empty = B == 0 || N == 0;
+  if (rot_dim > 0 && !empty && (rope == nullptr || positions == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(rope) || !aligned16(q_weight) || !aligned16(k_weight)) return ATTN_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(positions) & 3u) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * N > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  int at = 0;
+  for (int a = 0; a < num_axes; ++a) {
+    if (num_axes > 1) {
+      if (sections == nullptr || sections[a] < 0 || sections[a] > rot_dim / 2 - at) return ATTN_ERR_INVALID_ARG;
+      at += sections[a];
+    } else {
+      at = rot_dim / 2;
+    }
+    p.end[a] = at;
+  }
+  if (at != rot_dim / 2) return ATTN_ERR_INVALID_ARG;
+  p.w[0] = q_weight;
+  p.w[1] = k_weight;
+  p.rope = rope;
+  p.pos = positions;
+  p.axes = num_axes;
+  p.rot = rot_dim;
+  p.max_pos = max_pos;
+  p.B = B;
+  p.N = N;
+  p.H[0] = Hq;
+  p.H[1] = Hkv;
+  p.eps = eps;
+  return ATTN_OK;
+}
+
+// heads one warp takes: kUnroll loads of 32 / (d * size / 16) rows
+int qkn_heads(int d, int size) { return qkn::kUnroll * (512 / (d * size)); }
+
+template <bool kPaged>
+int launch_qkn(const qkn::Params& p, int dtype, int d, bool inter, cudaStream_t st) {
+  const int size = dtype == ATTN_DTYPE_BF16 ? 2 : 4;
+  const int heads = qkn_heads(d, size);
+  const long long chunks = (p.H[0] + heads - 1) / heads +
+                           static_cast<long long>(kPaged ? 2 : 1) * ((p.H[1] + heads - 1) / heads);
+  const long long blocks = (static_cast<long long>(p.B) * p.N * chunks + qkn::kWarps - 1) / qkn::kWarps;
+  if (blocks > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  void (*kern)(const qkn::Params) = nullptr;
+  using bf16 = __nv_bfloat16;
+  if (kPaged)
+    kern = inter ? qkn::qk_norm_rope_kernel<bf16, 128, true, kPaged> : qkn::qk_norm_rope_kernel<bf16, 128, false, kPaged>;
+  else if (dtype == ATTN_DTYPE_BF16 && d == 128)
+    kern = inter ? qkn::qk_norm_rope_kernel<bf16, 128, true, false> : qkn::qk_norm_rope_kernel<bf16, 128, false, false>;
+  else if (dtype == ATTN_DTYPE_BF16)
+    kern = inter ? qkn::qk_norm_rope_kernel<bf16, 64, true, false> : qkn::qk_norm_rope_kernel<bf16, 64, false, false>;
+  else if (d == 128)
+    kern = inter ? qkn::qk_norm_rope_kernel<float, 128, true, false> : qkn::qk_norm_rope_kernel<float, 128, false, false>;
+  else
+    kern = inter ? qkn::qk_norm_rope_kernel<float, 64, true, false> : qkn::qk_norm_rope_kernel<float, 64, false, false>;
+  kern<<<static_cast<unsigned>(blocks), qkn::kThreads, 0, st>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+// blocks of the backward pass, and rows of its partial weight gradients
+constexpr int kQknBwdBlocks = 148 * 3;
+
+bool page_size_ok(int page_size) {
+  return page_size >= 8 && page_size <= (1 << 20) && (page_size & (page_size - 1)) == 0;
+}
+int log2_int(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+// Decode behind shared prefixes: one CTA per SM of a B200, and the workspace is sized for that.
+constexpr int kPfxCtas = 148;
+
+struct PfxLayout {
+  long long own_row0, rows;
+  size_t lse_offset, plan_offset, total;
+};
+
+PfxLayout pfx_layout(int B, int Hq, int Hkv, int num_groups) {
+  PfxLayout L{};
+  const int G = Hq / Hkv;
+  L.own_row0 = 2ll * B * Hq + static_cast<long long>(kPfxCtas) * pfx::kCtaRows;
+  L.rows = L.own_row0 + 2ll * B * Hq + 2ll * G * kPfxCtas;
+  L.lse_offset = static_cast<size_t>(L.rows) * pfx::kD * sizeof(float);
+  L.plan_offset = (L.lse_offset + static_cast<size_t>(L.rows) * sizeof(float) + 15) & ~size_t(15);
+  L.total = L.plan_offset + (2 + static_cast<size_t>(num_groups) + B) * sizeof(int);
+  return L;
+}
+
+// Shapes that the prefix decode takes (the line of steps is counted in 32 bits).
+int pfx_shapes(int B, int Hq, int Hkv, int num_groups, int max_prefix_len, int max_seq_len, int d) {
+  if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || num_groups < 0 || max_prefix_len < 0 || max_seq_len < 0)
+    return ATTN_ERR_INVALID_ARG;
+  const int G = Hq / Hkv;
+  if (d != pfx::kD || (G != 1 && G != 2 && G != 4 && G != 8)) return ATTN_ERR_UNSUPPORTED;
+  const double blocks = std::min<double>(B, B / (256 / G) + static_cast<double>(num_groups));
+  const double cost = Hkv * (blocks * (max_prefix_len / 128 + 1.0) * pfx::kCostBoth + blocks * pfx::kCostJob +
+                             static_cast<double>(B) * ((max_seq_len / 128 + 1.0) * pfx::kCostAlt + pfx::kCostJob));
+  return cost < 2.0e9 ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
+
+int configure_pfx(DeviceInfo* info) {
+  int rc = configure_fwd(info);  // the tensor-map encoder
+  if (rc != ATTN_OK) return rc;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (!info->pfx_configured) {
+    for (auto* kern : {pfx::decode_prefix_kernel<false>, pfx::decode_prefix_kernel<true>}) {
+      rc = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            static_cast<int>(pfx::kSmemBytes)));
+      if (rc != ATTN_OK) return rc;
+    }
+    info->pfx_configured = true;
+  }
+  return ATTN_OK;
+}
+
+// [B][heads][128] queries of one token each, read as boxes of 64 columns x G heads x seqs sequences
+int encode_map_decode_q(CUtensorMap* map, const void* base, int heads, int B, int G, int seqs) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(pfx::kD), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pfx::kD) * 2,
+                                 static_cast<cuuint64_t>(heads) * pfx::kD * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(seqs)};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                        strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace attn
+
+extern "C" {
+
+int attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const void* q_weight,
+                      const void* k_weight, const float* rope, const int* positions,
+                      const long long* strides, const int* sections, int dtype, int B, int N, int Hq,
+                      int Hkv, int d, int rot_dim, int max_pos, int num_axes, int interleaved,
+                      float eps, attn_stream_t stream) {
+  qkn::Params p{};
+  int rc = qkn_common(p, q_weight, k_weight, rope, positions, sections, dtype, B, N, Hq, Hkv, d,
+                      rot_dim, max_pos, num_axes, eps);
+  if (rc != ATTN_OK) return rc;
+  if (strides == nullptr) return ATTN_ERR_INVALID_ARG;
+  const bool empty = B == 0 || N == 0;
+  if (!empty && (q == nullptr || k == nullptr || q_out == nullptr || k_out == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  const int size = dtype == ATTN_DTYPE_BF16 ? 2 : 4;
+  if (!view_ok(q, strides, B, Hq, N, size) || !view_ok(k, strides + 3, B, Hkv, N, size) ||
+      !view_ok(q_out, strides + 6, B, Hq, N, size) || !view_ok(k_out, strides + 9, B, Hkv, N, size))
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceInfo* info = nullptr;
+  if ((rc = current_device(&info)) != ATTN_OK) return rc;
+  if (empty) return ATTN_OK;
+  p.x[0] = q;
+  p.x[1] = k;
+  p.out[0] = q_out;
+  p.out[1] = k_out;
+  p.xs[0] = make_view(strides);
+  p.xs[1] = make_view(strides + 3);
+  p.os[0] = make_view(strides + 6);
+  p.os[1] = make_view(strides + 9);
+  p.pos_axis = strides[12];
+  p.pos_b = strides[13];
+  return launch_qkn<false>(p, dtype, d, interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int d) {
+  return d == 64 || d == 128 ? static_cast<size_t>(kQknBwdBlocks) * 2 * d * sizeof(float) : 0;
+}
+
+int attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                          void* dq, void* dk, const void* q_weight, const void* k_weight,
+                          float* dq_weight, float* dk_weight, const float* rope,
+                          const int* positions, const long long* strides, const int* sections,
+                          int dtype, int B, int N, int Hq, int Hkv, int d, int rot_dim, int max_pos,
+                          int num_axes, int interleaved, float eps, void* workspace,
+                          size_t workspace_bytes, attn_stream_t stream) {
+  qkn::Params p{};
+  int rc = qkn_common(p, q_weight, k_weight, rope, positions, sections, dtype, B, N, Hq, Hkv, d,
+                      rot_dim, max_pos, num_axes, eps);
+  if (rc != ATTN_OK) return rc;
+  if (strides == nullptr) return ATTN_ERR_INVALID_ARG;
+  const bool empty = B == 0 || N == 0;
+  if (!empty && (dq_out == nullptr || dk_out == nullptr || dq == nullptr || dk == nullptr ||
+                 (q_weight != nullptr && q == nullptr) || (k_weight != nullptr && k == nullptr)))
+    return ATTN_ERR_INVALID_ARG;
+  // a weight has a gradient, and only a weight has one
+  if ((q_weight == nullptr) != (dq_weight == nullptr) || (k_weight == nullptr) != (dk_weight == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  const int size = dtype == ATTN_DTYPE_BF16 ? 2 : 4;
+  if ((q_weight != nullptr && !view_ok(q, strides, B, Hq, N, size)) ||
+      (k_weight != nullptr && !view_ok(k, strides + 3, B, Hkv, N, size)) ||
+      !view_ok(dq_out, strides + 6, B, Hq, N, size) || !view_ok(dk_out, strides + 9, B, Hkv, N, size) ||
+      !view_ok(dq, strides + 12, B, Hq, N, size) || !view_ok(dk, strides + 15, B, Hkv, N, size))
+    return ATTN_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u)
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceInfo* info = nullptr;
+  if ((rc = current_device(&info)) != ATTN_OK) return rc;
+  const bool weighted = q_weight != nullptr || k_weight != nullptr;
+  if (weighted && (workspace == nullptr || !aligned16(workspace) ||
+                   workspace_bytes < attn_qk_norm_rope_bwd_workspace_bytes(d)))
+    return ATTN_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int blocks = 0;
+  if (!empty) {
+    p.x[0] = q;
+    p.x[1] = k;
+    p.dz[0] = dq_out;
+    p.dz[1] = dk_out;
+    p.out[0] = dq;
+    p.out[1] = dk;
+    p.xs[0] = make_view(strides);
+    p.xs[1] = make_view(strides + 3);
+    p.ds[0] = make_view(strides + 6);
+    p.ds[1] = make_view(strides + 9);
+    p.os[0] = make_view(strides + 12);
+    p.os[1] = make_view(strides + 15);
+    p.pos_axis = strides[18];
+    p.pos_b = strides[19];
+    p.dw = static_cast<float*>(workspace);
+    const int heads = qkn_heads(d, size);
+    const long long chunks = (Hq + heads - 1) / heads + static_cast<long long>((Hkv + heads - 1) / heads);
+    const long long want = (static_cast<long long>(B) * N * chunks + qkn::kWarps - 1) / qkn::kWarps;
+    blocks = static_cast<int>(std::min<long long>(want, kQknBwdBlocks));
+    using bf16 = __nv_bfloat16;
+    void (*kern)(const qkn::Params) = nullptr;
+    if (dtype == ATTN_DTYPE_BF16 && d == 128)
+      kern = interleaved ? qkn::qk_norm_rope_bwd_kernel<bf16, 128, true> : qkn::qk_norm_rope_bwd_kernel<bf16, 128, false>;
+    else if (dtype == ATTN_DTYPE_BF16)
+      kern = interleaved ? qkn::qk_norm_rope_bwd_kernel<bf16, 64, true> : qkn::qk_norm_rope_bwd_kernel<bf16, 64, false>;
+    else if (d == 128)
+      kern = interleaved ? qkn::qk_norm_rope_bwd_kernel<float, 128, true> : qkn::qk_norm_rope_bwd_kernel<float, 128, false>;
+    else
+      kern = interleaved ? qkn::qk_norm_rope_bwd_kernel<float, 64, true> : qkn::qk_norm_rope_bwd_kernel<float, 64, false>;
+    kern<<<static_cast<unsigned>(blocks), qkn::kThreads, 0, st>>>(p);
+    if ((rc = cuda_status(cudaGetLastError())) != ATTN_OK) return rc;
+  }
+  if (weighted) {
+    qkn::qk_norm_dw_kernel<<<dim3(d / 32, 2), 1024, 0, st>>>(static_cast<const float*>(workspace),
+                                                             blocks, d, dq_weight, dk_weight);
+    rc = cuda_status(cudaGetLastError());
+  }
+  return rc;
+}
+
+int attn_qk_norm_rope_paged(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                            void* v_cache, const void* q_weight, const void* k_weight,
+                            const float* rope, const int* positions, const int* slots,
+                            const long long* strides, const int* sections, int T, int Hq, int Hkv,
+                            int num_pages, int page_size, int d, int rot_dim, int max_pos,
+                            int num_axes, int interleaved, float eps, attn_stream_t stream) {
+  qkn::Params p{};
+  int rc = qkn_common(p, q_weight, k_weight, rope, positions, sections, ATTN_DTYPE_BF16, 1, T, Hq,
+                      Hkv, d, rot_dim, max_pos, num_axes, eps);
+  if (rc != ATTN_OK) return rc;
+  if (strides == nullptr || num_pages < 0 || !page_size_ok(page_size)) return ATTN_ERR_INVALID_ARG;
+  if (d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (T > 0 && (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr || slots == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  if (T > 0 && num_pages > 0 && (k_cache == nullptr || v_cache == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (!view_ok(q, strides, 1, Hq, T, 2) || !view_ok(k, strides + 3, 1, Hkv, T, 2) ||
+      !view_ok(v, strides + 6, 1, Hkv, T, 2) || !view_ok(q_out, strides + 9, 1, Hq, T, 2) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || (reinterpret_cast<uintptr_t>(slots) & 3u))
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceInfo* info = nullptr;
+  if ((rc = current_device(&info)) != ATTN_OK) return rc;
+  if (T == 0) return ATTN_OK;
+  p.x[0] = q;
+  p.x[1] = k;
+  p.v = v;
+  p.out[0] = q_out;
+  p.xs[0] = make_view(strides);
+  p.xs[1] = make_view(strides + 3);
+  p.vs = make_view(strides + 6);
+  p.os[0] = make_view(strides + 9);
+  p.pos_axis = strides[12];
+  p.pos_b = 0;
+  p.slots = slots;
+  p.cache[0] = k_cache;
+  p.cache[1] = v_cache;
+  p.slots_total = num_pages * page_size;
+  return launch_qkn<true>(p, ATTN_DTYPE_BF16, d, interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_page_update(int* block_table, const int* old_lens, const int* new_lens, int* free_pages,
+                     const long long* ring_in, long long* ring_out, int* cu_seqlens, int* slots,
+                     int* positions, const int* pos_offset, int B, int max_pages_per_seq,
+                     int page_size, int num_pages, int max_tokens, attn_stream_t stream) {
+  if (B < 0 || max_pages_per_seq < 0 || num_pages < 0 || max_tokens < 0 || !page_size_ok(page_size))
+    return ATTN_ERR_INVALID_ARG;
+  if (ring_in == nullptr || ring_out == nullptr || cu_seqlens == nullptr ||
+      (B > 0 && (old_lens == nullptr || new_lens == nullptr)) ||
+      (B > 0 && max_pages_per_seq > 0 && block_table == nullptr) ||
+      (num_pages > 0 && free_pages == nullptr) ||
+      (max_tokens > 0 && (slots == nullptr || positions == nullptr)))
+    return ATTN_ERR_INVALID_ARG;
+  // the blocks read one ring state while one of them writes the other
+  if (ring_in < ring_out + 3 && ring_out < ring_in + 3) return ATTN_ERR_INVALID_ARG;
+  if (B > pages::kMaxRequests || static_cast<long long>(num_pages) * page_size > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(ring_in) | reinterpret_cast<uintptr_t>(ring_out)) & 7u) return ATTN_ERR_UNSUPPORTED;
+  DeviceInfo* info = nullptr;
+  int rc = current_device(&info);
+  if (rc != ATTN_OK) return rc;
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!info->pages_configured) {
+      rc = cuda_status(cudaFuncSetAttribute(pages::page_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            (3 * pages::kMaxRequests + 1) * static_cast<int>(sizeof(int))));
+      if (rc != ATTN_OK) return rc;
+      info->pages_configured = true;
+    }
+  }
+  pages::Params p{};
+  p.table = block_table;
+  p.old_lens = old_lens;
+  p.new_lens = new_lens;
+  p.free_pages = free_pages;
+  p.ring_in = ring_in;
+  p.ring_out = ring_out;
+  p.cu = cu_seqlens;
+  p.slots = slots;
+  p.positions = positions;
+  p.offset = pos_offset;
+  p.B = B;
+  p.max_pages = max_pages_per_seq;
+  p.page_shift = log2_int(page_size);
+  p.cap = num_pages;
+  p.max_tokens = max_tokens;
+  const int want = std::max((max_tokens - 1) / pages::kThreads + 1, (B + pages::kWarps - 1) / pages::kWarps);
+  const int blocks = std::max(1, std::min(want, info->num_sms));
+  const size_t smem = (3 * static_cast<size_t>(B) + 1) * sizeof(int);
+  pages::page_update_kernel<<<blocks, pages::kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+size_t attn_decode_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int num_groups,
+                                                 int max_prefix_len, int max_seq_len, int d) {
+  if (pfx_shapes(B, Hq, Hkv, num_groups, max_prefix_len, max_seq_len, d) != ATTN_OK) return 0;
+  return pfx_layout(B, Hq, Hkv, num_groups).total;
+}
+
+int attn_decode_shared_prefix(const void* q, const void* k_cache, const void* v_cache, void* o,
+                              float* lse, const int* prefix_table, const int* prefix_lens,
+                              const int* group_starts, const int* block_table, const int* seq_lens,
+                              int B, int Hq, int Hkv, int num_groups, int num_pages, int page_size,
+                              int max_prefix_pages, int max_prefix_len, int max_pages_per_seq,
+                              int max_seq_len, int d, float scale, void* workspace,
+                              size_t workspace_bytes, attn_stream_t stream) {
+  int rc = pfx_shapes(B, Hq, Hkv, num_groups, max_prefix_len, max_seq_len, d);
+  if (rc != ATTN_OK) return rc;
+  if (num_pages < 0 || max_prefix_pages < 0 || max_pages_per_seq < 0 || !page_size_ok(page_size))
+    return ATTN_ERR_INVALID_ARG;
+  if (max_prefix_len > static_cast<long long>(max_prefix_pages) * page_size ||
+      max_seq_len > static_cast<long long>(max_pages_per_seq) * page_size)
+    return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  const bool prefixes = num_groups > 0 && max_prefix_len > 0, own = max_seq_len > 0;
+  if (B > 0) {
+    if (q == nullptr || o == nullptr) return ATTN_ERR_INVALID_ARG;
+    if ((prefixes || own) && num_pages > 0 && (k_cache == nullptr || v_cache == nullptr)) return ATTN_ERR_INVALID_ARG;
+    if (num_groups > 0 && (prefix_lens == nullptr || group_starts == nullptr)) return ATTN_ERR_INVALID_ARG;
+    if (prefixes && prefix_table == nullptr) return ATTN_ERR_INVALID_ARG;
+    if (seq_lens == nullptr || (own && block_table == nullptr)) return ATTN_ERR_INVALID_ARG;
+  }
+  if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_UNSUPPORTED;
+  if (lse != nullptr && (reinterpret_cast<uintptr_t>(lse) & 3u)) return ATTN_ERR_UNSUPPORTED;
+  DeviceInfo* info = nullptr;
+  if ((rc = current_device(&info)) != ATTN_OK) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (B == 0) return ATTN_OK;
+  if (!prefixes && !own)
+    return launch_fill_empty(static_cast<__nv_bfloat16*>(o), lse, static_cast<size_t>(B) * Hq, d, st);
+  if (num_pages == 0) return ATTN_ERR_INVALID_ARG;  // keys, but no page to hold one
+  const PfxLayout L = pfx_layout(B, Hq, Hkv, num_groups);
+  if (workspace == nullptr || workspace_bytes < L.total || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+  if ((rc = configure_pfx(info)) != ATTN_OK) return rc;
+
+  pfx::Params p{};
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.S = 128 / p.G;
+  p.num_groups = prefixes ? num_groups : 0;
+  p.max_prefix_len = max_prefix_len;
+  p.max_prefix_pages = max_prefix_pages;
+  p.max_seq_len = max_seq_len;
+  p.max_pages = max_pages_per_seq;
+  p.num_pages = num_pages;
+  p.page_shift = log2_int(page_size);
+  p.prefix_table = prefix_table;
+  p.prefix_lens = prefix_lens;
+  p.group_starts = group_starts;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  // scale = 0 makes every weight equal; a tiny positive c gives exactly that (see attn_fwd)
+  p.c = scale * kLog2e;
+  if (p.c == 0.f) p.c = 1e-30f;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.lse_offset);
+  p.plan = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + L.plan_offset);
+  p.own_row0 = L.own_row0;
+
+  CUtensorMap tq, tq_own, tk, tv;
+  const int rows = num_pages * page_size;
+  const uint32_t piece = static_cast<uint32_t>(std::min(page_size, pfx::kTile));
+  if (encode_map_decode_q(&tq, q, Hq, B, p.G, p.S) != ATTN_OK ||
+      encode_map_decode_q(&tq_own, q, Hq, B, p.G, 1) != ATTN_OK ||
+      encode_map_packed(&tk, k_cache, rows, Hkv, piece) != ATTN_OK ||
+      encode_map_packed(&tv, v_cache, rows, Hkv, piece) != ATTN_OK)
+    return ATTN_ERR_UNSUPPORTED;
+  const int ctas = std::min(info->num_sms, kPfxCtas);
+  if (scale < 0.f)
+    pfx::decode_prefix_kernel<true><<<ctas, pfx::kThreads, pfx::kSmemBytes, st>>>(tq, tq_own, tk, tv, p);
+  else
+    pfx::decode_prefix_kernel<false><<<ctas, pfx::kThreads, pfx::kSmemBytes, st>>>(tq, tq_own, tk, tv, p);
+  if ((rc = cuda_status(cudaGetLastError())) != ATTN_OK) return rc;
+  const long long rows_out = static_cast<long long>(B) * Hq;
+  pfx::decode_prefix_combine_kernel<<<static_cast<unsigned>((rows_out + pfx::kCombineWarps - 1) / pfx::kCombineWarps),
+                                      pfx::kCombineWarps * 32, 0, st>>>(p, static_cast<__nv_bfloat16*>(o), lse);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

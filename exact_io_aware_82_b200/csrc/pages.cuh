@@ -1,0 +1,168 @@
+// Bookkeeping of a paged KV cache on the device: from the lengths of the requests before and after
+// a step, the pages each request takes from or returns to the pool, its block table row, and the
+// cache slot and position of every new token.
+//
+// Request b holds had = ceil(old / page) pages and needs need = ceil(new / page).  With
+//   grow_b = max(need - had, 0),  shrink_b = max(had - need, 0),  tokens_b = max(new - old, 0)
+// and their exclusive sums G, S, T over the requests:
+//   table[b][had + j]             = free[(head + G_b + j) mod cap]     for j < grow_b
+//   free[(tail + S_b + j) mod cap] = table[b][need + j]                for j < shrink_b
+//   token t of request b is at p = old + t - T_b:  slot = page(p / page) * page + p % page.
+// The free pages are a ring, so pages taken and pages returned never touch the same entries and
+// the step needs no order between the two.
+//
+// Bound by latency: a step of 64 requests moves a few KB.  So it is one launch without any
+// communication between blocks: every block sums all requests for itself (three sums in one scan,
+// the results kept in shared memory) and then takes its share of the rows and of the tokens; a
+// token that falls into a page taken in this very step reads it from the ring, not from the
+// table row another block is writing.
+#pragma once
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace attn {
+namespace pages {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxRequests = 16384;  // three sums per request in shared memory
+
+struct Params {
+  int* table;           // [B][max_pages]
+  const int* old_lens;  // [B]
+  const int* new_lens;  // [B]
+  int* free_pages;      // [cap]
+  const long long* ring_in;  // head, tail, -
+  long long* ring_out;       // head, tail, pages missing (-1: invalid arguments)
+  int* cu;              // [B + 1]
+  int* slots;           // [max_tokens]
+  int* positions;       // [max_tokens]
+  const int* offset;    // [B] or null
+  int B, max_pages, page_shift, cap, max_tokens;
+};
+
+struct Sums {
+  long long grow, shrink, tokens;
+};
+
+__device__ __forceinline__ int pages_of(int len, int shift) {
+  return static_cast<int>((static_cast<long long>(len) + (1 << shift) - 1) >> shift);
+}
+
+__global__ void __launch_bounds__(kThreads) page_update_kernel(const Params p) {
+  extern __shared__ int smem[];
+  int* cu = smem;                // [B + 1] first token of each request
+  int* grow0 = cu + p.B + 1;     // [B] pages taken by the requests before
+  int* shrink0 = grow0 + p.B;    // [B] pages returned by the requests before
+  __shared__ Sums warp_sums[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long max_len = static_cast<long long>(p.max_pages) << p.page_shift;
+
+  // each thread sums a run of requests, the block scans the threads' sums
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int first = min(tid * per, p.B), last = min(first + per, p.B);
+  Sums mine{0, 0, 0};
+  bool bad = false;
+  for (int b = first; b < last; ++b) {
+    const int a = __ldg(p.old_lens + b), n = __ldg(p.new_lens + b);
+    bad = bad || a < 0 || n < 0 || a > max_len || n > max_len;
+    const int d = pages_of(n, p.page_shift) - pages_of(a, p.page_shift);
+    mine.grow += max(d, 0);
+    mine.shrink += max(-d, 0);
+    mine.tokens += max(n - a, 0);
+  }
+  bad = __syncthreads_or(bad) != 0;
+  Sums run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, run.grow, o);
+    const long long y = __shfl_up_sync(0xffffffffu, run.shrink, o);
+    const long long z = __shfl_up_sync(0xffffffffu, run.tokens, o);
+    if (lane >= o) run.grow += x, run.shrink += y, run.tokens += z;
+  }
+  if (lane == 31) warp_sums[warp] = run;
+  __syncthreads();
+  Sums all{0, 0, 0}, before{0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const Sums s = warp_sums[w];
+    if (w < warp) before.grow += s.grow, before.shrink += s.shrink, before.tokens += s.tokens;
+    all.grow += s.grow, all.shrink += s.shrink, all.tokens += s.tokens;
+  }
+  const long long head = p.ring_in[0], tail = p.ring_in[1], held = tail - head;
+  bad = bad || head < 0 || held < 0 || held > p.cap || held + all.shrink > p.cap ||
+        all.tokens > p.max_tokens;
+  const long long missing = bad ? -1 : max(all.grow - held, 0ll);
+  if (blockIdx.x == 0 && tid == 0) {
+    p.ring_out[0] = missing == 0 ? head + all.grow : head;
+    p.ring_out[1] = missing == 0 ? tail + all.shrink : tail;
+    p.ring_out[2] = missing;
+    if (bad) atomicExch(&g_device_error, ATTN_ERR_INVALID_ARG);
+  }
+  const int threads = gridDim.x * kThreads, gtid = blockIdx.x * kThreads + tid;
+  if (missing != 0) {
+    // all or nothing: the tables, the ring and its ends stay as they were, no token has a slot
+    for (int b = gtid; b <= p.B; b += threads) p.cu[b] = 0;
+    for (int t = gtid; t < p.max_tokens; t += threads) p.slots[t] = -1, p.positions[t] = 0;
+    return;
+  }
+  {
+    // the sums are now known to fit: tokens <= max_tokens, pages <= cap
+    int g = static_cast<int>(before.grow + run.grow - mine.grow);
+    int s = static_cast<int>(before.shrink + run.shrink - mine.shrink);
+    int t = static_cast<int>(before.tokens + run.tokens - mine.tokens);
+    for (int b = first; b < last; ++b) {
+      const int a = __ldg(p.old_lens + b), n = __ldg(p.new_lens + b);
+      const int d = pages_of(n, p.page_shift) - pages_of(a, p.page_shift);
+      cu[b] = t, grow0[b] = g, shrink0[b] = s;
+      g += max(d, 0), s += max(-d, 0), t += max(n - a, 0);
+    }
+    if (tid == 0) cu[p.B] = static_cast<int>(all.tokens);
+  }
+  __syncthreads();
+  for (int b = gtid; b <= p.B; b += threads) p.cu[b] = cu[b];
+
+  const int head0 = static_cast<int>(p.cap > 0 ? head % p.cap : 0);
+  const int tail0 = static_cast<int>(p.cap > 0 ? tail % p.cap : 0);
+  // entry `at` places behind `from` in the ring (both below cap)
+  auto ring = [&](int from, int at) {
+    const long long i = static_cast<long long>(from) + at;
+    return static_cast<int>(i >= p.cap ? i - p.cap : i);
+  };
+  // block table rows: a warp per request
+  for (int b = blockIdx.x * kWarps + warp; b < p.B; b += gridDim.x * kWarps) {
+    const int had = pages_of(__ldg(p.old_lens + b), p.page_shift);
+    const int need = pages_of(__ldg(p.new_lens + b), p.page_shift);
+    int* row = p.table + static_cast<size_t>(b) * p.max_pages;
+    for (int j = lane; j < need - had; j += 32) row[had + j] = p.free_pages[ring(head0, grow0[b] + j)];
+    for (int j = lane; j < had - need; j += 32) p.free_pages[ring(tail0, shrink0[b] + j)] = row[need + j];
+  }
+  // tokens: a thread per token
+  for (int t = gtid; t < p.max_tokens; t += threads) {
+    int slot = -1, pos = 0;
+    if (t < cu[p.B]) {
+      int lo = 0, hi = p.B;  // the last request with cu[lo] <= t
+      while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (cu[m] <= t) lo = m;
+        else hi = m;
+      }
+      const int a = __ldg(p.old_lens + lo), at = a + (t - cu[lo]);
+      const int had = pages_of(a, p.page_shift), i = at >> p.page_shift;
+      const int page = i < had ? p.table[static_cast<size_t>(lo) * p.max_pages + i]
+                               : p.free_pages[ring(head0, grow0[lo] + i - had)];
+      if (page >= 0 && page < p.cap)
+        slot = (page << p.page_shift) + (at & ((1 << p.page_shift) - 1));
+      else
+        atomicExch(&g_device_error, ATTN_ERR_INVALID_ARG);
+      pos = at + (p.offset != nullptr ? __ldg(p.offset + lo) : 0);
+    }
+    p.slots[t] = slot;
+    p.positions[t] = pos;
+  }
+}
+
+}  // namespace pages
+}  // namespace attn

@@ -44,7 +44,7 @@
  * when a launch itself failed).  Device-side waits are bounded; if one expires the kernel
  * stops early, records the event in a device flag and `attn_get_device_error` reports
  * ATTN_ERR_DEVICE_TIMEOUT after the stream has been synchronised (the same flag reports an
- * out-of-range page number met by attn_decode_paged).
+ * out-of-range page number, position or cache slot met by the paged and norm + rotation calls).
  */
 #ifndef EXACT_ATTN_B200_ATTN_H
 #define EXACT_ATTN_B200_ATTN_H
@@ -70,6 +70,12 @@ enum attn_mask_kind {
   ATTN_MASK_CAUSAL = 1,
   ATTN_MASK_SLIDING = 2,
   ATTN_MASK_LOCAL_GLOBAL = 3
+};
+
+/* Element type of the calls that take more than one. */
+enum attn_dtype {
+  ATTN_DTYPE_BF16 = 0,
+  ATTN_DTYPE_F32 = 1
 };
 
 enum attn_status {
@@ -284,13 +290,162 @@ ATTN_API int attn_decode_noalloc(const void *q, const void *k, const void *v, vo
                                  int B, int Hq, int Hkv, int Nk, int d, float scale,
                                  int num_splits, attn_stream_t stream);
 
+/*
+ * attn_qk_norm_rope - queries and keys on their way from the projection to attention: every row of d
+ * values is normalised by its root mean square, weighted, and rotated by its token's position.
+ * For a row x of token (b, n) with weight w:
+ *     r = 1 / sqrt(mean(x^2) + eps),   y_i = x_i r w_i   (y = x where the weight is NULL),
+ *     z_lo = y_lo cos - y_hi sin,   z_hi = y_hi cos + y_lo sin   for each rotated pair,
+ * and z = y in the columns from rot_dim on.  Pair i of the rot_dim / 2 pairs is columns
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved != 0; cos = rope[pos][i], sin =
+ * rope[pos][rot_dim / 2 + i] with the token's position on the pair's axis.
+ *   q, q_out  [B][Hq][N][d];  k, k_out  [B][Hkv][N][d], all of `dtype` (attn_dtype), as views with d
+ *             contiguous and the strides below; packed sequences are B = 1, N = tokens.  An output may
+ *             be its input (same address and strides); otherwise the two must not overlap.
+ *   q_weight, k_weight  [d] of `dtype`, each NULL where that side is not normalised.
+ *   rope      fp32 [max_pos][rot_dim] (may be NULL when rot_dim == 0).
+ *   positions int32 [num_axes][B][N] (axis and batch strides below; 0 shares one row).  A position
+ *             outside [0, max_pos) is not followed: its pairs are left unrotated, and the device flag
+ *             records ATTN_ERR_INVALID_ARG.
+ *   strides   HOST long long [14], in elements: (b, h, n) of q, k, q_out, k_out, then the axis and
+ *             the batch stride of positions.
+ *   sections  HOST int [num_axes]: pairs rotated by each axis, in order, together rot_dim / 2
+ *             (time, height and width of image and video tokens, for instance); not read when
+ *             num_axes == 1.
+ *   d in {64, 128}; 0 <= rot_dim <= d, a multiple of 16; 1 <= num_axes <= 4; eps finite, >= 0.
+ *   Row addresses are multiples of 16 bytes (ATTN_ERR_UNSUPPORTED otherwise), strides included.
+ *   All arithmetic is fp32, the output is rounded once.
+ */
+ATTN_API int attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
+                               const void *q_weight, const void *k_weight, const float *rope,
+                               const int *positions, const long long *strides, const int *sections,
+                               int dtype, int B, int N, int Hq, int Hkv, int d, int rot_dim,
+                               int max_pos, int num_axes, int interleaved, float eps,
+                               attn_stream_t stream);
+
+/*
+ * attn_qk_norm_rope_bwd - gradient of attn_qk_norm_rope: from dq_out, dk_out (dL/dz) and the call's
+ * inputs, dq, dk (dL/dx) and the weights' gradients.  With dy = the transposed rotation of dz and
+ * g = dy w:   dx = r (g - x r^2 mean(g x)),   dw = sum over all rows of dy x r.
+ *   q, dq_out, dq  [B][Hq][N][d];  k, dk_out, dk  [B][Hkv][N][d] views; q (k) may be NULL where its
+ *             weight is.  dq may be dq_out or q in place (same address and strides), likewise dk.
+ *   dq_weight, dk_weight  fp32 [d], given exactly where the weight is; fully written.
+ *   strides   HOST long long [20]: (b, h, n) of q, k, dq_out, dk_out, dq, dk, then of positions as
+ *             above.
+ *   workspace device scratch of at least attn_qk_norm_rope_bwd_workspace_bytes(d) bytes, 16-byte
+ *             aligned, overwritten before it is read (needed where a weight is given).
+ * Other arguments and rules as attn_qk_norm_rope.  Weight gradients are summed in fp32 in an order
+ * that the shapes fix (no atomics).
+ */
+ATTN_API size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
+
+ATTN_API int attn_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out,
+                                   const void *dk_out, void *dq, void *dk, const void *q_weight,
+                                   const void *k_weight, float *dq_weight, float *dk_weight,
+                                   const float *rope, const int *positions, const long long *strides,
+                                   const int *sections, int dtype, int B, int N, int Hq, int Hkv,
+                                   int d, int rot_dim, int max_pos, int num_axes, int interleaved,
+                                   float eps, void *workspace, size_t workspace_bytes,
+                                   attn_stream_t stream);
+
+/*
+ * attn_qk_norm_rope_paged - attn_qk_norm_rope for serving: queries of T packed tokens go to q_out,
+ * keys (normalised and rotated) and values (as they are) into the paged cache that
+ * attn_decode_paged and attn_decode_shared_prefix read.  bf16, d == 128.
+ *   q, q_out  [T][Hq][d];  k, v  [T][Hkv][d] views;  positions int32 [num_axes][T].
+ *   k_cache, v_cache  bf16 [num_pages][page_size][Hkv][d], contiguous; page_size as attn_decode_paged.
+ *   slots     int32 [T]: token t is written to row slots[t] of the cache's num_pages * page_size rows.
+ *             A token with a negative slot is left out (nothing of it is read or written, q_out
+ *             included): the padding of a fixed token count.  A slot past the cache is not followed
+ *             either, and the device flag records ATTN_ERR_INVALID_ARG.  Slots of one call are
+ *             distinct; of two tokens with one slot, which one the row ends with is not specified.
+ *   strides   HOST long long [13]: (unused, h, t) of q, k, v, q_out, then the axis stride of positions.
+ * Other arguments and rules as attn_qk_norm_rope; rows of the cache that no slot names stay as they are.
+ */
+ATTN_API int attn_qk_norm_rope_paged(const void *q, const void *k, const void *v, void *q_out,
+                                     void *k_cache, void *v_cache, const void *q_weight,
+                                     const void *k_weight, const float *rope, const int *positions,
+                                     const int *slots, const long long *strides, const int *sections,
+                                     int T, int Hq, int Hkv, int num_pages, int page_size, int d,
+                                     int rot_dim, int max_pos, int num_axes, int interleaved,
+                                     float eps, attn_stream_t stream);
+
+/*
+ * attn_page_update - the bookkeeping of a paged cache for one step, on the device: from every
+ * request's length before and after it, the pages taken from and returned to the pool, the block
+ * tables, and where each new token goes.  A request grows (a prompt, a decode step), shrinks
+ * (rejected tokens; to 0: it has ended) or stays.
+ *   block_table  int32 [B][max_pages_per_seq], updated: page i of request b holds its keys
+ *                [i page_size, (i + 1) page_size).  Entries past the last page are not touched when a
+ *                request shrinks and never read.
+ *   old_lens, new_lens  int32 [B], each in [0, max_pages_per_seq * page_size].
+ *   free_pages   int32 [num_pages], updated: a ring of free page numbers.  With h = head and t =
+ *                tail, its entries h, h + 1, ..., t - 1 (mod num_pages) are free; pages are taken at
+ *                the head, in request order, and returned at the tail, in request order.  A page
+ *                returned by a call can be taken by the next one.
+ *   ring_in, ring_out  int64 [3]: head, tail (both count up without wrapping) and the pages missing;
+ *                ring_in[2] is not read.  Two different arrays.
+ *   cu_seqlens   int32 [B + 1]: request b's new tokens are [cu_seqlens[b], cu_seqlens[b + 1]), as
+ *                attn_fwd_varlen takes them (none for a request that shrinks).
+ *   slots, positions  int32 [max_tokens]: the cache row (attn_qk_norm_rope_paged's slots) and the
+ *                position of every new token, position = its place in the request + pos_offset[b]
+ *                (pos_offset int32 [B] or NULL: the shared prefix before the request's own keys);
+ *                behind the last token -1 and 0.
+ *   B <= 16384 and num_pages * page_size < 2^31 (else ATTN_ERR_UNSUPPORTED); page_size as
+ *   attn_decode_paged.
+ * All or nothing: where the free pages do not suffice, ring_out[2] is the number missing, and where
+ * a length, the ring or the number of new tokens (more than max_tokens) is not valid it is -1 and
+ * the device flag records ATTN_ERR_INVALID_ARG; either way ring_out keeps head and tail, tables and
+ * ring stay as they were, cu_seqlens and positions are 0 and slots -1.  A page number outside the
+ * pool that a token falls into gives the slot -1 and is flagged.
+ */
+ATTN_API int attn_page_update(int *block_table, const int *old_lens, const int *new_lens,
+                              int *free_pages, const long long *ring_in, long long *ring_out,
+                              int *cu_seqlens, int *slots, int *positions, const int *pos_offset,
+                              int B, int max_pages_per_seq, int page_size, int num_pages,
+                              int max_tokens, attn_stream_t stream);
+
+/*
+ * attn_decode_shared_prefix - decode for a batch whose sequences share prefixes (a system prompt, a
+ * document, the prompt of several sampled answers): a prefix's keys are read and multiplied once
+ * for all sequences behind it, and the result is that of attn_decode_paged on prefix + own keys.
+ *   q, o, k_cache, v_cache, block_table, seq_lens, max_seq_len, page_size  as attn_decode_paged, with
+ *                block_table and seq_lens for a sequence's own keys (those after the prefix).
+ *   lse          fp32 [B][Hq] or NULL, over prefix and own keys.
+ *   group_starts int32 [num_groups + 1] (device), non-decreasing: sequences [group_starts[g],
+ *                group_starts[g + 1]) share prefix g; sequences before the first and from the last
+ *                entry on have none.  Clamped to [0, B].
+ *   prefix_table int32 [num_groups][max_prefix_pages], prefix_lens int32 [num_groups]: the pages and
+ *                the keys of each prefix, in the same cache; lengths are clamped on the device to
+ *                [0, max_prefix_len], and max_prefix_len must not exceed max_prefix_pages * page_size.
+ *   A sequence with no key at all gets O = 0, LSE = -inf.  What a page holds behind a sequence's (or
+ *   prefix's) last key is not used, infinities and NaN included.
+ *   workspace    device scratch of at least attn_decode_shared_prefix_workspace_bytes(...) bytes,
+ *                16-byte aligned, overwritten before it is read.
+ * G = Hq / Hkv in {1, 2, 4, 8}, d == 128.  Errors, and page numbers outside the cache, as
+ * attn_decode_paged.  The result does not depend on scheduling (no atomics, no counter: captured
+ * graphs with workspaces of their own may run at the same time).
+ */
+ATTN_API size_t attn_decode_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int num_groups,
+                                                          int max_prefix_len, int max_seq_len, int d);
+
+ATTN_API int attn_decode_shared_prefix(const void *q, const void *k_cache, const void *v_cache,
+                                       void *o, float *lse, const int *prefix_table,
+                                       const int *prefix_lens, const int *group_starts,
+                                       const int *block_table, const int *seq_lens, int B, int Hq,
+                                       int Hkv, int num_groups, int num_pages, int page_size,
+                                       int max_prefix_pages, int max_prefix_len,
+                                       int max_pages_per_seq, int max_seq_len, int d, float scale,
+                                       void *workspace, size_t workspace_bytes,
+                                       attn_stream_t stream);
+
 /* The split count attn_decode uses for num_splits = 0 on the current device. */
 ATTN_API int attn_decode_num_splits(int B, int Hq, int Hkv, int Nk, int d);
 
 /*
  * Reads and clears the device error flag of the current device after synchronising `stream`.
  * Returns ATTN_OK, ATTN_ERR_DEVICE_TIMEOUT (a bounded wait expired), ATTN_ERR_INVALID_ARG (a
- * paged decode met a page number outside its cache), or ATTN_ERR_CUDA if the synchronisation
+ * kernel met a page number, position, slot or length that it refused to follow), or ATTN_ERR_CUDA if the synchronisation
  * failed.
  */
 ATTN_API int attn_get_device_error(attn_stream_t stream);
