@@ -1135,35 +1135,50 @@ int qkn_common(qkn::Params& p, const void* q_weight, const void* k_weight, const
   return ATTN_OK;
 }
 
-// heads one warp takes: kUnroll loads of 32 / (d * size / 16) rows
-int qkn_heads(int d, int size) { return qkn::kUnroll * (512 / (d * size)); }
+// Warps of a norm + rotation call: every item (a warp's heads of one token) of its own, up to a grid of
+// per_sm blocks per SM (what its registers allow), and at least one warp for every group of heads.
+int qkn_blocks(const qkn::Params& p, int d, int size, int unroll, bool paged, int grid, long long* blocks) {
+  const int heads = unroll * (512 / (d * size));
+  const long long chunks = (p.H[0] + heads - 1) / heads +
+                           static_cast<long long>(paged ? 2 : 1) * ((p.H[1] + heads - 1) / heads);
+  const long long want = (static_cast<long long>(p.B) * p.N * chunks + qkn::kWarps - 1) / qkn::kWarps;
+  const long long least = (chunks + qkn::kWarps - 1) / qkn::kWarps;
+  *blocks = std::max(std::min<long long>(want, grid), least);
+  return *blocks <= (1 << 20) ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
 
 template <bool kPaged>
-int launch_qkn(const qkn::Params& p, int dtype, int d, bool inter, cudaStream_t st) {
-  const int size = dtype == ATTN_DTYPE_BF16 ? 2 : 4;
-  const int heads = qkn_heads(d, size);
-  const long long chunks = (p.H[0] + heads - 1) / heads +
-                           static_cast<long long>(kPaged ? 2 : 1) * ((p.H[1] + heads - 1) / heads);
-  const long long blocks = (static_cast<long long>(p.B) * p.N * chunks + qkn::kWarps - 1) / qkn::kWarps;
-  if (blocks > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+int launch_qkn(const qkn::Params& p, int dtype, int d, bool inter, int num_sms, cudaStream_t st) {
+  long long blocks = 0;
+  int rc = qkn_blocks(p, d, dtype == ATTN_DTYPE_BF16 ? 2 : 4, qkn::kUnroll, kPaged, qkn::kBlocks * num_sms, &blocks);
+  if (rc != ATTN_OK) return rc;
   void (*kern)(const qkn::Params) = nullptr;
   using bf16 = __nv_bfloat16;
-  if (kPaged)
-    kern = inter ? qkn::qk_norm_rope_kernel<bf16, 128, true, kPaged> : qkn::qk_norm_rope_kernel<bf16, 128, false, kPaged>;
-  else if (dtype == ATTN_DTYPE_BF16 && d == 128)
-    kern = inter ? qkn::qk_norm_rope_kernel<bf16, 128, true, false> : qkn::qk_norm_rope_kernel<bf16, 128, false, false>;
-  else if (dtype == ATTN_DTYPE_BF16)
-    kern = inter ? qkn::qk_norm_rope_kernel<bf16, 64, true, false> : qkn::qk_norm_rope_kernel<bf16, 64, false, false>;
-  else if (d == 128)
-    kern = inter ? qkn::qk_norm_rope_kernel<float, 128, true, false> : qkn::qk_norm_rope_kernel<float, 128, false, false>;
-  else
-    kern = inter ? qkn::qk_norm_rope_kernel<float, 64, true, false> : qkn::qk_norm_rope_kernel<float, 64, false, false>;
+  const bool full = p.rot == d, multi = p.axes > 1;
+#define ATTN_QKN_PICK(T, D)                                                                             \
+  kern = full ? (multi ? (inter ? qkn::qk_norm_rope_kernel<T, D, true, true, true, kPaged>                \
+                                : qkn::qk_norm_rope_kernel<T, D, false, true, true, kPaged>)              \
+                       : (inter ? qkn::qk_norm_rope_kernel<T, D, true, true, false, kPaged>               \
+                                : qkn::qk_norm_rope_kernel<T, D, false, true, false, kPaged>))            \
+              : (multi ? (inter ? qkn::qk_norm_rope_kernel<T, D, true, false, true, kPaged>               \
+                                : qkn::qk_norm_rope_kernel<T, D, false, false, true, kPaged>)             \
+                       : (inter ? qkn::qk_norm_rope_kernel<T, D, true, false, false, kPaged>              \
+                                : qkn::qk_norm_rope_kernel<T, D, false, false, false, kPaged>))
+  if constexpr (kPaged) {
+    ATTN_QKN_PICK(bf16, 128);
+  } else {
+    if (dtype == ATTN_DTYPE_BF16 && d == 128) ATTN_QKN_PICK(bf16, 128);
+    else if (dtype == ATTN_DTYPE_BF16) ATTN_QKN_PICK(bf16, 64);
+    else if (d == 128) ATTN_QKN_PICK(float, 128);
+    else ATTN_QKN_PICK(float, 64);
+  }
+#undef ATTN_QKN_PICK
   kern<<<static_cast<unsigned>(blocks), qkn::kThreads, 0, st>>>(p);
   return cuda_status(cudaGetLastError());
 }
 
 // blocks of the backward pass, and rows of its partial weight gradients
-constexpr int kQknBwdBlocks = 148 * 3;
+constexpr int kQknBwdBlocks = 148 * qkn::kBlocksBwd;
 
 bool page_size_ok(int page_size) {
   return page_size >= 8 && page_size <= (1 << 20) && (page_size & (page_size - 1)) == 0;
@@ -1270,7 +1285,8 @@ int attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, co
   p.os[1] = make_view(strides + 9);
   p.pos_axis = strides[12];
   p.pos_b = strides[13];
-  return launch_qkn<false>(p, dtype, d, interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
+  return launch_qkn<false>(p, dtype, d, interleaved != 0, info->num_sms,
+                           reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t attn_qk_norm_rope_bwd_workspace_bytes(int d) {
@@ -1327,21 +1343,28 @@ int attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, cons
     p.os[1] = make_view(strides + 15);
     p.pos_axis = strides[18];
     p.pos_b = strides[19];
-    p.dw = static_cast<float*>(workspace);
-    const int heads = qkn_heads(d, size);
-    const long long chunks = (Hq + heads - 1) / heads + static_cast<long long>((Hkv + heads - 1) / heads);
-    const long long want = (static_cast<long long>(B) * N * chunks + qkn::kWarps - 1) / qkn::kWarps;
-    blocks = static_cast<int>(std::min<long long>(want, kQknBwdBlocks));
+    p.dw = weighted ? static_cast<float*>(workspace) : nullptr;
+    long long want = 0;
+    if ((rc = qkn_blocks(p, d, size, qkn::kUnrollBwd, false, kQknBwdBlocks, &want)) != ATTN_OK) return rc;
+    if (want > kQknBwdBlocks) return ATTN_ERR_UNSUPPORTED;  // more heads than the partial rows' warps
+    blocks = static_cast<int>(want);
     using bf16 = __nv_bfloat16;
     void (*kern)(const qkn::Params) = nullptr;
-    if (dtype == ATTN_DTYPE_BF16 && d == 128)
-      kern = interleaved ? qkn::qk_norm_rope_bwd_kernel<bf16, 128, true> : qkn::qk_norm_rope_bwd_kernel<bf16, 128, false>;
-    else if (dtype == ATTN_DTYPE_BF16)
-      kern = interleaved ? qkn::qk_norm_rope_bwd_kernel<bf16, 64, true> : qkn::qk_norm_rope_bwd_kernel<bf16, 64, false>;
-    else if (d == 128)
-      kern = interleaved ? qkn::qk_norm_rope_bwd_kernel<float, 128, true> : qkn::qk_norm_rope_bwd_kernel<float, 128, false>;
-    else
-      kern = interleaved ? qkn::qk_norm_rope_bwd_kernel<float, 64, true> : qkn::qk_norm_rope_bwd_kernel<float, 64, false>;
+    const bool full = rot_dim == d, multi = num_axes > 1, inter = interleaved != 0;
+#define ATTN_QKN_PICK(T, D)                                                                             \
+  kern = full ? (multi ? (inter ? qkn::qk_norm_rope_bwd_kernel<T, D, true, true, true>                    \
+                                : qkn::qk_norm_rope_bwd_kernel<T, D, false, true, true>)                  \
+                       : (inter ? qkn::qk_norm_rope_bwd_kernel<T, D, true, true, false>                   \
+                                : qkn::qk_norm_rope_bwd_kernel<T, D, false, true, false>))                \
+              : (multi ? (inter ? qkn::qk_norm_rope_bwd_kernel<T, D, true, false, true>                   \
+                                : qkn::qk_norm_rope_bwd_kernel<T, D, false, false, true>)                 \
+                       : (inter ? qkn::qk_norm_rope_bwd_kernel<T, D, true, false, false>                  \
+                                : qkn::qk_norm_rope_bwd_kernel<T, D, false, false, false>))
+    if (dtype == ATTN_DTYPE_BF16 && d == 128) ATTN_QKN_PICK(bf16, 128);
+    else if (dtype == ATTN_DTYPE_BF16) ATTN_QKN_PICK(bf16, 64);
+    else if (d == 128) ATTN_QKN_PICK(float, 128);
+    else ATTN_QKN_PICK(float, 64);
+#undef ATTN_QKN_PICK
     kern<<<static_cast<unsigned>(blocks), qkn::kThreads, 0, st>>>(p);
     if ((rc = cuda_status(cudaGetLastError())) != ATTN_OK) return rc;
   }
@@ -1390,7 +1413,8 @@ int attn_qk_norm_rope_paged(const void* q, const void* k, const void* v, void* q
   p.cache[0] = k_cache;
   p.cache[1] = v_cache;
   p.slots_total = num_pages * page_size;
-  return launch_qkn<true>(p, ATTN_DTYPE_BF16, d, interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
+  return launch_qkn<true>(p, ATTN_DTYPE_BF16, d, interleaved != 0, info->num_sms,
+                           reinterpret_cast<cudaStream_t>(stream));
 }
 
 int attn_page_update(int* block_table, const int* old_lens, const int* new_lens, int* free_pages,

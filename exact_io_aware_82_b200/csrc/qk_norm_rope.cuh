@@ -13,10 +13,15 @@
 //   dx = r (g - x r^2 mean(g x)),   dw = sum over rows of dy x r.
 //
 // Bound by HBM: a row is read once and written once (the backward pass reads x and dz), all sums
-// are fp32 in registers, the one rounding is the output's.  A lane holds 16 bytes of a row, so a
-// bf16 row of 128 is 16 lanes and a warp-wide load is two whole rows; a warp takes kUnroll such
-// loads of one token at once (every load is issued before the first is used) and reuses the
-// token's table columns for all of them.
+// are fp32 in registers, the one rounding is the output's.  What keeps a kernel of this kind from
+// the memory's rate is its instructions, and the layout of a row over lanes follows from that:
+//   - a lane holds 16 bytes of a row as two halves A and B: kH columns and their kH partners (i and
+//     i + rot_dim / 2), or 2 kH adjacent columns when interleaved, so a pair never leaves its lane;
+//   - a warp takes the same heads of every step-th token: weights stay in registers, the token's
+//     table columns are loaded once for kUnroll row loads, addresses advance by additions;
+//   - the kUnroll row sums are reduced together (each step of the exchange halves the values a lane
+//     still carries), so r is computed once per row instead of once per lane and row;
+//   - arithmetic is in pairs of fp32 values.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -30,7 +35,10 @@ namespace qkn {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 4;     // row loads of a warp's item, forward
+constexpr int kUnrollBwd = 2;  // backward: of x and of dz
+constexpr int kBlocks = 3;     // per SM, forward: 80 registers a thread
+constexpr int kBlocksBwd = 2;  // per SM, backward
 constexpr int kMaxAxes = 4;
 
 // Element strides of a [B][H][N][d] view (d contiguous).
@@ -52,7 +60,7 @@ struct Params {
   int B, N, H[2];
   float eps;
   float* dw;  // backward: partial weight gradients [blocks][2][d]
-  // paged form: x[2..] are the values; tokens with a negative slot are left out
+  // paged form: the values, and tokens with a negative slot are left out
   const void* v;
   View vs;
   const int* slots;
@@ -60,353 +68,534 @@ struct Params {
   int slots_total;
 };
 
-// 16 bytes of a row as fp32
-template <typename T>
-struct Vec;
-template <>
-struct Vec<__nv_bfloat16> {
-  static constexpr int kN = 8;
-  static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    return make_uint4(dev::pack_bf16x2(f[0], f[1]), dev::pack_bf16x2(f[2], f[3]),
-                      dev::pack_bf16x2(f[4], f[5]), dev::pack_bf16x2(f[6], f[7]));
-  }
-};
-template <>
-struct Vec<float> {
-  static constexpr int kN = 4;
-  static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
-    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
-  }
-};
-
-// not the read-only path: the forward pass may run in place
-__device__ __forceinline__ uint4 load16(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p)
-               : "memory");
-  return r;
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t z;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(dev::pack2(a.x, a.y)), "l"(dev::pack2(b.x, b.y)));
+  return dev::unpack2(z);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  return dev::unpack2(dev::fma2(dev::pack2(a.x, a.y), dev::pack2(b.x, b.y), dev::pack2(c.x, c.y)));
 }
 
-// The part of the row that lane `sub` of its row's lanes holds, and its partner's.
-template <typename T, int D, bool kInter>
+// One half of a lane's 16 bytes as fp32 pairs
+template <typename T>
+struct Half;
+template <>
+struct Half<__nv_bfloat16> {
+  static constexpr int kH = 4, kP = 2;  // columns, pairs of columns
+  static __device__ __forceinline__ void unpack(uint32_t a, uint32_t b, float2 (&f)[2]) {
+    f[0] = make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+    f[1] = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint2 pack(const float2 (&f)[2]) {
+    return make_uint2(dev::pack_bf16x2(f[0].x, f[0].y), dev::pack_bf16x2(f[1].x, f[1].y));
+  }
+};
+template <>
+struct Half<float> {
+  static constexpr int kH = 2, kP = 1;
+  static __device__ __forceinline__ void unpack(uint32_t a, uint32_t b, float2 (&f)[1]) {
+    f[0] = make_float2(__uint_as_float(a), __uint_as_float(b));
+  }
+  static __device__ __forceinline__ uint2 pack(const float2 (&f)[1]) {
+    return make_uint2(__float_as_uint(f[0].x), __float_as_uint(f[0].y));
+  }
+};
+
+// A lane's place in its row.  kFull: rot_dim == d.
+template <typename T, int D, bool kInter, bool kFull>
 struct Lane {
-  static constexpr int kV = Vec<T>::kN;
-  static constexpr int kLanes = D / kV;      // lanes of a row
-  static constexpr int kRows = 32 / kLanes;  // rows of a warp-wide load
-  int sub, col, row;
-  int partner;  // lane that holds the other half of this lane's pairs
-  int sign;     // of the sine: -1 first half, +1 second half, 0 not rotated
-  int pair;     // first pair
+  static constexpr int kH = Half<T>::kH, kP = Half<T>::kP;
+  static constexpr int kLanes = D / (2 * kH);  // lanes of a row
+  static constexpr int kRows = 32 / kLanes;    // rows of a warp-wide load
+  int row, sub;
+  int col, gap;  // first column of A, columns from A to B
+  bool turned;   // the lane's columns are rotated
   __device__ __forceinline__ explicit Lane(int rot) {
     const int lane = threadIdx.x & 31;
-    sub = lane % kLanes;
     row = lane / kLanes;
-    col = sub * kV;
-    partner = lane;
-    sign = 0;
-    pair = 0;
-    if (col < rot) {
-      if (kInter) {
-        pair = col / 2;
-        sign = 1;
-      } else {
-        const int half = rot / 2;
-        sign = col < half ? -1 : 1;
-        pair = col < half ? col : col - half;
-        partner = col < half ? lane + half / kV : lane - half / kV;
-      }
+    sub = lane % kLanes;
+    turned = kFull || sub < rot / (2 * kH);
+    col = (!kInter && turned ? kH : 2 * kH) * sub;
+    gap = kInter || !turned ? kH : kFull ? D / 2 : rot / 2;
+  }
+  __device__ __forceinline__ int pair() const { return kH * sub; }
+  __device__ __forceinline__ uint4 load(const T* p) const {
+    uint4 r;
+    // not the read-only path: the forward pass may run in place
+    if constexpr (kInter) {
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    } else {
+      asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p) : "memory");
+      asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                   : "=r"(r.z), "=r"(r.w) : "l"(p + gap) : "memory");
+    }
+    return r;
+  }
+  __device__ __forceinline__ void store(T* p, uint2 a, uint2 b) const {
+    if constexpr (kInter) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      *reinterpret_cast<uint2*>(p) = a;
+      *reinterpret_cast<uint2*>(p + gap) = b;
     }
   }
-  // column of the pair partner of element e
-  __device__ __forceinline__ int partner_col(int e, int rot) const {
-    if (sign == 0) return col + e;
-    if (kInter) return col + (e ^ 1);
-    return col + e + (sign < 0 ? rot / 2 : -rot / 2);
+  // weights of the lane's columns (1 without)
+  __device__ __forceinline__ void weights(const T* w, float2 (&a)[kP], float2 (&b)[kP]) const {
+#pragma unroll
+    for (int e = 0; e < kP; ++e) {
+      a[e] = b[e] = make_float2(1.f, 1.f);
+      if (w != nullptr) {
+        const T* wa = w + col + 2 * e;
+        a[e] = make_float2(static_cast<float>(wa[0]), static_cast<float>(wa[1]));
+        b[e] = make_float2(static_cast<float>(wa[gap]), static_cast<float>(wa[gap + 1]));
+      }
+    }
   }
 };
 
-// cos and signed sin of this lane's columns for token (b, n).
-template <typename T, int D, bool kInter>
-__device__ __forceinline__ void load_angles(const Params& p, const Lane<T, D, kInter>& ln, int b,
-                                            int n, float (&c)[Vec<T>::kN], float (&s)[Vec<T>::kN]) {
-  constexpr int kV = Vec<T>::kN;
-  constexpr int kPairs = kInter ? kV / 2 : kV;
-#pragma unroll
-  for (int e = 0; e < kV; ++e) c[e] = 1.f, s[e] = 0.f;
-  if (ln.sign == 0) return;
-  const int* pos = p.pos + b * p.pos_b + n;
-  int at[kMaxAxes];
-  bool in[kMaxAxes];
-#pragma unroll
-  for (int a = 0; a < kMaxAxes; ++a) {
-    at[a] = a < p.axes ? __ldg(pos + a * p.pos_axis) : 0;
-    in[a] = at[a] >= 0 && at[a] < p.max_pos;
-  }
-  float cc[kPairs], ss[kPairs];
-  bool bad = false;
-  auto axis_of = [&](int pair) {
-    int a = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxAxes - 1; ++i)
-      if (i + 1 < p.axes && pair >= p.end[i]) a = i + 1;
-    return a;
-  };
-  auto pick = [&](int a) { return a == 0 ? at[0] : a == 1 ? at[1] : a == 2 ? at[2] : at[3]; };
-  auto okay = [&](int a) { return a == 0 ? in[0] : a == 1 ? in[1] : a == 2 ? in[2] : in[3]; };
-  constexpr int kStep = kPairs >= 4 ? 4 : kPairs;
-#pragma unroll
-  for (int i = 0; i < kPairs; i += kStep) {
-    const int a0 = axis_of(ln.pair + i), a1 = axis_of(ln.pair + i + kStep - 1);
-    if (a0 == a1) {
-      const float* row = p.rope + static_cast<size_t>(okay(a0) ? pick(a0) : 0) * p.rot + ln.pair + i;
-      if (!okay(a0)) {
-        bad = true;
-#pragma unroll
-        for (int e = 0; e < kStep; ++e) cc[i + e] = 1.f, ss[i + e] = 0.f;
-      } else if constexpr (kStep == 4) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(row));
-        const float4 y = __ldg(reinterpret_cast<const float4*>(row + p.rot / 2));
-        cc[i] = x.x, cc[i + 1] = x.y, cc[i + 2] = x.z, cc[i + 3] = x.w;
-        ss[i] = y.x, ss[i + 1] = y.y, ss[i + 2] = y.z, ss[i + 3] = y.w;
-      } else {
-        const float2 x = __ldg(reinterpret_cast<const float2*>(row));
-        const float2 y = __ldg(reinterpret_cast<const float2*>(row + p.rot / 2));
-        cc[i] = x.x, cc[i + 1] = x.y;
-        ss[i] = y.x, ss[i + 1] = y.y;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kStep; ++e) {
-        const int a = axis_of(ln.pair + i + e);
-        const float* row = p.rope + static_cast<size_t>(okay(a) ? pick(a) : 0) * p.rot + ln.pair + i + e;
-        bad = bad || !okay(a);
-        cc[i + e] = okay(a) ? __ldg(row) : 1.f;
-        ss[i + e] = okay(a) ? __ldg(row + p.rot / 2) : 0.f;
-      }
-    }
-  }
-  // a position outside the table is not followed: its pairs are not rotated, and it is flagged
-  if (bad) atomicExch(&g_device_error, ATTN_ERR_INVALID_ARG);
-#pragma unroll
-  for (int e = 0; e < kV; ++e) {
-    c[e] = cc[kInter ? e / 2 : e];
-    const float sn = ss[kInter ? e / 2 : e];
-    s[e] = kInter ? ((e & 1) ? sn : -sn) : (ln.sign < 0 ? -sn : sn);
-  }
-}
-
-// the values of each lane's pair partners
-template <typename T, bool kInter>
-__device__ __forceinline__ void partners(const uint4& raw, int lane, float (&f)[Vec<T>::kN]) {
-  if (kInter) {
-    float g[Vec<T>::kN];
-    Vec<T>::unpack(raw, g);
-#pragma unroll
-    for (int e = 0; e < Vec<T>::kN; ++e) f[e] = g[e ^ 1];
-  } else {
-    uint4 u;
-    u.x = __shfl_sync(0xffffffffu, raw.x, lane);
-    u.y = __shfl_sync(0xffffffffu, raw.y, lane);
-    u.z = __shfl_sync(0xffffffffu, raw.z, lane);
-    u.w = __shfl_sync(0xffffffffu, raw.w, lane);
-    Vec<T>::unpack(u, f);
-  }
-}
-
-template <int kLanes>
-__device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-// A warp's item: kHeads heads of one token, all queries, all keys or all values.
-template <typename T, int D, bool kInter, bool kPaged>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const Params p) {
-  using L = Lane<T, D, kInter>;
-  constexpr int kV = L::kV;
-  constexpr int kHeads = kUnroll * L::kRows;
-  const L ln(p.rot);
-  const int cq = (p.H[0] + kHeads - 1) / kHeads, ck = (p.H[1] + kHeads - 1) / kHeads;
-  const int chunks = cq + (kPaged ? 2 : 1) * ck;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const long long token = item / chunks;
-  const int chunk = static_cast<int>(item % chunks);
-  if (token >= static_cast<long long>(p.B) * p.N) return;
-  const int b = static_cast<int>(token / p.N), n = static_cast<int>(token % p.N);
-  const int kind = chunk < cq ? 0 : chunk < cq + ck ? 1 : 2;  // queries, keys, values
-  const int side = kind == 0 ? 0 : 1;
-  const int h0 = (chunk - (kind == 0 ? 0 : kind == 1 ? cq : cq + ck)) * kHeads + ln.row;
-  const int H = p.H[side];
-  long long slot = 0;
-  if (kPaged) {
-    slot = __ldg(p.slots + token);
-    if (slot < 0) return;
-    if (slot >= p.slots_total) {
-      atomicExch(&g_device_error, ATTN_ERR_INVALID_ARG);
+// A token's positions, one per axis (kMulti) or the only one.
+template <bool kMulti>
+struct Pos {
+  int at[kMulti ? kMaxAxes : 1];
+  __device__ __forceinline__ void load(const Params& p, int b, int n) {
+    if (p.rot == 0) {
+      at[0] = 0;
       return;
     }
-  }
-  const View& xs = (kPaged && kind == 2) ? p.vs : p.xs[side];
-  const T* x = static_cast<const T*>((kPaged && kind == 2) ? p.v : p.x[side]) + b * xs.b + n * xs.n + ln.col;
-  T* out;
-  long long oh;
-  if (kPaged && kind != 0) {
-    out = static_cast<T*>(p.cache[kind - 1]) + slot * p.H[1] * D + ln.col;
-    oh = D;
-  } else {
-    out = static_cast<T*>(p.out[side]) + b * p.os[side].b + n * p.os[side].n + ln.col;
-    oh = p.os[side].h;
-  }
-  uint4 raw[kUnroll];
+    const int* pos = p.pos + b * p.pos_b + n;
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int h = h0 + u * L::kRows;
-    raw[u] = h < H ? load16(x + h * xs.h) : make_uint4(0u, 0u, 0u, 0u);
+    for (int a = 0; a < (kMulti ? kMaxAxes : 1); ++a)
+      at[a] = (!kMulti || a < p.axes) ? __ldg(pos + a * p.pos_axis) : 0;
   }
-  if (kPaged && kind == 2) {
+  __device__ __forceinline__ int pick(int a) const {
+    if constexpr (kMulti)
+      return a == 0 ? at[0] : a == 1 ? at[1] : a == 2 ? at[2] : at[3];
+    else
+      return at[0];
+  }
+};
+
+__device__ __forceinline__ int axis_of(const Params& p, int pair) {
+  int a = 0;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * L::kRows;
-      if (h < H) *reinterpret_cast<uint4*>(out + h * oh) = raw[u];
+  for (int i = 0; i < kMaxAxes - 1; ++i)
+    if (i + 1 < p.axes && pair >= p.end[i]) a = i + 1;
+  return a;
+}
+
+// cos and sin of this lane's kH pairs.  A position outside the table is not followed: its pairs are
+// not rotated, and it is flagged.
+template <typename T, int D, bool kInter, bool kFull, bool kMulti>
+struct Angles {
+  using L = Lane<T, D, kInter, kFull>;
+  static constexpr int kH = L::kH, kP = L::kP;
+  float c[kH], s[kH];
+  __device__ __forceinline__ void load(const Params& p, const L& ln, const Pos<kMulti>& pos) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kH; ++i) c[i] = 1.f, s[i] = 0.f;
+    if (ln.turned) {
+      const int rot = kFull ? D : p.rot;
+      const int a0 = kMulti ? axis_of(p, ln.pair()) : 0;
+      if (!kMulti || a0 == axis_of(p, ln.pair() + kH - 1)) {
+        const int at = pos.pick(a0);
+        bad = at < 0 || at >= p.max_pos;
+        if (!bad) {
+          const float* row = p.rope + static_cast<size_t>(at) * rot + ln.pair();
+          if constexpr (kH == 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(row));
+            const float4 y = __ldg(reinterpret_cast<const float4*>(row + rot / 2));
+            c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w;
+            s[0] = y.x, s[1] = y.y, s[2] = y.z, s[3] = y.w;
+          } else {
+            const float2 x = __ldg(reinterpret_cast<const float2*>(row));
+            const float2 y = __ldg(reinterpret_cast<const float2*>(row + rot / 2));
+            c[0] = x.x, c[1] = x.y;
+            s[0] = y.x, s[1] = y.y;
+          }
+        }
+      } else {  // the border of two sections
+#pragma unroll
+        for (int e = 0; e < kH; ++e) {
+          const int at = pos.pick(axis_of(p, ln.pair() + e));
+          if (at >= 0 && at < p.max_pos) {
+            const float* row = p.rope + static_cast<size_t>(at) * rot + ln.pair() + e;
+            c[e] = __ldg(row);
+            s[e] = __ldg(row + rot / 2);
+          } else {
+            bad = true;
+          }
+        }
+      }
     }
-    return;
+    if (bad) atomicExch(&g_device_error, ATTN_ERR_INVALID_ARG);
   }
-  const T* w = static_cast<const T*>(p.w[side]);
-  float wc[kV], ws[kV];
-  load_angles<T, D, kInter>(p, ln, b, n, wc, ws);
-  if (w != nullptr) {
-#pragma unroll
-    for (int e = 0; e < kV; ++e) {
-      wc[e] *= static_cast<float>(w[ln.col + e]);
-      ws[e] *= static_cast<float>(w[ln.partner_col(e, p.rot)]);
+  // (cos, cos) and (-sin, sin) of the columns that pair of columns e of half A / B stands for
+  __device__ __forceinline__ float2 cosine(bool second, int e) const {
+    if constexpr (kInter) {
+      const float x = second ? c[kP + e] : c[e];
+      return make_float2(x, x);
+    } else {
+      return make_float2(c[2 * e], c[2 * e + 1]);
     }
   }
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    float f[kV], g[kV];
-    Vec<T>::unpack(raw[u], f);
-    partners<T, kInter>(raw[u], ln.partner, g);
-    float r = 1.f;
-    if (w != nullptr) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < kV; ++e) ss = fmaf(f[e], f[e], ss);
-      r = rsqrtf(row_sum<L::kLanes>(ss) * (1.f / D) + p.eps);
+  __device__ __forceinline__ float2 sine(bool second, int e) const {
+    if constexpr (kInter) {
+      const float x = second ? s[kP + e] : s[e];
+      return make_float2(-x, x);
+    } else {
+      return second ? make_float2(s[2 * e], s[2 * e + 1]) : make_float2(-s[2 * e], -s[2 * e + 1]);
     }
-    // a column that is not rotated keeps its own value alone: no 0 x partner
+  }
+};
+
+__device__ __forceinline__ float2 swap2(float2 x) { return make_float2(x.y, x.x); }
+
+// f = f cf + partner sf for both halves (partner: the other half, or the neighbour when interleaved).
+// A lane that is not rotated keeps f cf alone: no 0 x partner.
+template <typename L, bool kInter, bool kFull>
+__device__ __forceinline__ void turn(const L& ln, float2 (&a)[L::kP], float2 (&b)[L::kP],
+                                     const float2 (&ca)[L::kP], const float2 (&sa)[L::kP],
+                                     const float2 (&cb)[L::kP], const float2 (&sb)[L::kP]) {
 #pragma unroll
-    for (int e = 0; e < kV; ++e)
-      f[e] = r * (ln.sign == 0 ? f[e] * wc[e] : fmaf(g[e], ws[e], f[e] * wc[e]));
-    const int h = h0 + u * L::kRows;
-    if (h < H) *reinterpret_cast<uint4*>(out + h * oh) = Vec<T>::pack(f);
+  for (int e = 0; e < L::kP; ++e) {
+    const float2 pa = kInter ? swap2(a[e]) : b[e], pb = kInter ? swap2(b[e]) : a[e];
+    const float2 ya = mul2(a[e], ca[e]), yb = mul2(b[e], cb[e]);
+    const float2 za = fma2(pa, sa[e], ya), zb = fma2(pb, sb[e], yb);
+    a[e] = kFull || ln.turned ? za : ya;
+    b[e] = kFull || ln.turned ? zb : yb;
   }
 }
 
-// Backward: persistent blocks; every warp takes items of the queries, then of the keys, and keeps
-// the weight gradient of its columns in registers on the way; a block adds its warps' up in a fixed
-// order and writes one partial row per side.
-template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const Params p) {
-  using L = Lane<T, D, kInter>;
-  constexpr int kV = L::kV;
-  constexpr int kHeads = kUnroll * L::kRows;
-  __shared__ float red[kWarps * L::kRows][D];
-  const L ln(p.rot);
-  const int warp = threadIdx.x >> 5;
-  const long long tokens = static_cast<long long>(p.B) * p.N;
-  for (int side = 0; side < 2; ++side) {
-    const int H = p.H[side];
-    const int chunks = (H + kHeads - 1) / kHeads;
-    const T* w = static_cast<const T*>(p.w[side]);
-    float wt[kV], dw[kV];
+// Sums of four values over the kLanes lanes of a row; the lane ends with the sum of value
+// 2 * (its bit kLanes / 2) + (its bit kLanes / 4).
+template <int kLanes>
+__device__ __forceinline__ float sum4(float v0, float v1, float v2, float v3) {
+  const int lane = threadIdx.x & 31;
+  const bool hi = lane & (kLanes / 2), odd = lane & (kLanes / 4);
+  const float a = (hi ? v2 : v0) + __shfl_xor_sync(0xffffffffu, hi ? v0 : v2, kLanes / 2);
+  const float b = (hi ? v3 : v1) + __shfl_xor_sync(0xffffffffu, hi ? v1 : v3, kLanes / 2);
+  float x = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, kLanes / 4);
 #pragma unroll
-    for (int e = 0; e < kV; ++e) {
-      wt[e] = w != nullptr ? static_cast<float>(w[ln.col + e]) : 1.f;
-      dw[e] = 0.f;
+  for (int o = kLanes / 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// the value that sum4's lane for value i holds
+template <int kLanes>
+__device__ __forceinline__ float from4(float x, int i) {
+  const int base = threadIdx.x & (32 - kLanes);
+  return __shfl_sync(0xffffffffu, x, base + (i >> 1) * (kLanes / 2) + (i & 1) * (kLanes / 4));
+}
+
+// Which heads and tokens a warp takes: the same heads (queries, keys or values) of every step-th
+// token, with the token's place (b, n) and its offsets kept up by additions.
+struct Walk {
+  int kind, h0, left;    // left: tokens from the current one to the end
+  int step, step_b, step_n;
+  int b, n;
+  __device__ __forceinline__ Walk(const Params& p, int heads, bool paged) {
+    const int cq = (p.H[0] + heads - 1) / heads, ck = (p.H[1] + heads - 1) / heads;
+    const int chunks = cq + (paged ? 2 : 1) * ck;
+    const int warps = gridDim.x * kWarps, w = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    step = warps / chunks;  // the launch has chunks warps at least
+    const int token = w / chunks, chunk = w % chunks;
+    left = token < step ? p.B * p.N - token : 0;
+    kind = chunk < cq ? 0 : chunk < cq + ck ? 1 : 2;
+    h0 = (chunk - (kind == 0 ? 0 : kind == 1 ? cq : cq + ck)) * heads;
+    b = token / p.N;
+    n = token % p.N;
+    step_b = step / p.N;
+    step_n = step % p.N;
+  }
+  __device__ __forceinline__ bool live() const { return left > 0; }
+  __device__ __forceinline__ void next(const Params& p) {
+    left -= step;
+    b += step_b;
+    n += step_n;
+    if (n >= p.N) {
+      n -= p.N;
+      ++b;
     }
-    for (long long item = static_cast<long long>(blockIdx.x) * kWarps + warp; item < tokens * chunks;
-         item += static_cast<long long>(gridDim.x) * kWarps) {
-      const long long token = item / chunks;
-      const int h0 = static_cast<int>(item % chunks) * kHeads + ln.row;
-      const int b = static_cast<int>(token / p.N), n = static_cast<int>(token % p.N);
-      const View xs = p.xs[side], ds = p.ds[side], os = p.os[side];
-      const T* x = static_cast<const T*>(p.x[side]) + b * xs.b + n * xs.n + ln.col;
-      const T* dz = static_cast<const T*>(p.dz[side]) + b * ds.b + n * ds.n + ln.col;
-      T* dx = static_cast<T*>(p.out[side]) + b * os.b + n * os.n + ln.col;
-      uint4 rx[kUnroll], rz[kUnroll];
+  }
+};
+
+// Strides that every token needs again: kept in shared memory and read there each time, so that they
+// do not hold registers through the loop (the loops below run at 80 registers, three blocks per SM).
+struct Strides {
+  long long b, n;
+  __device__ __forceinline__ void set(const View& v) volatile { b = v.b, n = v.n; }
+  __device__ __forceinline__ long long at(int ib, int in) const volatile { return ib * b + in * n; }
+};
+
+// Forward.
+template <typename T, int D, bool kInter, bool kFull, bool kMulti, bool kPaged>
+__global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_kernel(const Params p) {
+  using L = Lane<T, D, kInter, kFull>;
+  constexpr int kP = L::kP;
+  __shared__ volatile Strides st[3][2];  // of a kind's input and output
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) st[i][0].set(p.xs[i]), st[i][1].set(p.os[i]);
+    st[2][0].set(p.vs);
+  }
+  __syncthreads();
+  const L ln(p.rot);
+  Walk wk(p, kUnroll * L::kRows, kPaged);
+  if (!wk.live()) return;
+  const int side = wk.kind == 0 ? 0 : 1;
+  const bool copy = kPaged && wk.kind == 2;      // values: as they are
+  const bool to_cache = kPaged && wk.kind != 0;
+  const int h0 = wk.h0 + ln.row, H = p.H[side];
+  const View& xs = copy ? p.vs : p.xs[side];
+  const View& os = p.os[side];
+  const T* x0 = static_cast<const T*>(copy ? p.v : p.x[side]) + h0 * xs.h + ln.col;
+  T* out0 = to_cache ? static_cast<T*>(p.cache[wk.kind - 1]) + h0 * D + ln.col
+                     : static_cast<T*>(p.out[side]) + h0 * os.h + ln.col;
+  const long long xh = xs.h * L::kRows, oh = (to_cache ? D : os.h) * L::kRows;
+  const T* w = copy ? nullptr : static_cast<const T*>(p.w[side]);
+  float2 wa[kP], wb[kP];
+  ln.weights(w, wa, wb);
+  // the cache slot of the walk's token (below 0: left out)
+  auto slot_of = [&](const Walk& k) -> int {
+    if (!kPaged) return 0;
+    const int s = __ldg(p.slots + k.n);
+    if (s < p.slots_total) return s;
+    atomicExch(&g_device_error, ATTN_ERR_INVALID_ARG);
+    return -1;
+  };
+  Pos<kMulti> pos;
+  if (!copy) pos.load(p, wk.b, wk.n);
+  int slot = slot_of(wk);
+  while (true) {
+    const int b = wk.b, n = wk.n, cur = slot;
+    const Pos<kMulti> cur_pos = pos;
+    wk.next(p);
+    const bool on = !kPaged || cur >= 0;
+    uint4 raw[kUnroll];
+    if (on) {
+      const T* x = x0 + st[wk.kind][0].at(b, n);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int h = h0 + u * L::kRows;
-        rx[u] = rz[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < H) {
-          rz[u] = load16(dz + h * ds.h);
-          if (w != nullptr) rx[u] = load16(x + h * xs.h);
+      for (int u = 0; u < kUnroll; ++u)
+        raw[u] = h0 + u * L::kRows < H ? ln.load(x + u * xh) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    // the next token's position and slot are on their way meanwhile
+    if (wk.live()) {
+      if (!copy) pos.load(p, wk.b, wk.n);
+      slot = slot_of(wk);
+    }
+    if (on) {
+      T* out = to_cache ? out0 + static_cast<long long>(cur) * p.H[1] * D : out0 + st[wk.kind][1].at(b, n);
+      if (copy) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (h0 + u * L::kRows < H)
+            ln.store(out + u * oh, make_uint2(raw[u].x, raw[u].y), make_uint2(raw[u].z, raw[u].w));
+      } else {
+        Angles<T, D, kInter, kFull, kMulti> ang;
+        ang.load(p, ln, cur_pos);
+        // angle times weight: the column's own, and the partner's
+        float2 ca[kP], sa[kP], cb[kP], sb[kP];
+#pragma unroll
+        for (int e = 0; e < kP; ++e) {
+          ca[e] = mul2(wa[e], ang.cosine(false, e));
+          cb[e] = mul2(wb[e], ang.cosine(true, e));
+          sa[e] = mul2(kInter ? swap2(wa[e]) : wb[e], ang.sine(false, e));
+          sb[e] = mul2(kInter ? swap2(wb[e]) : wa[e], ang.sine(true, e));
+        }
+        float r4 = 1.f;
+        if (w != nullptr) {
+          float ss[kUnroll];
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) {
+            float2 fa[kP], fb[kP];
+            Half<T>::unpack(raw[u].x, raw[u].y, fa);
+            Half<T>::unpack(raw[u].z, raw[u].w, fb);
+            float2 t = mul2(fa[0], fa[0]);
+#pragma unroll
+            for (int e = 1; e < kP; ++e) t = fma2(fa[e], fa[e], t);
+#pragma unroll
+            for (int e = 0; e < kP; ++e) t = fma2(fb[e], fb[e], t);
+            ss[u] = t.x + t.y;
+          }
+          r4 = rsqrtf(sum4<L::kLanes>(ss[0], ss[1], ss[2], ss[3]) * (1.f / D) + p.eps);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const float r = from4<L::kLanes>(r4, u);
+          const float2 rr = make_float2(r, r);
+          float2 fa[kP], fb[kP];
+          Half<T>::unpack(raw[u].x, raw[u].y, fa);
+          Half<T>::unpack(raw[u].z, raw[u].w, fb);
+          turn<L, kInter, kFull>(ln, fa, fb, ca, sa, cb, sb);
+#pragma unroll
+          for (int e = 0; e < kP; ++e) fa[e] = mul2(fa[e], rr), fb[e] = mul2(fb[e], rr);
+          if (h0 + u * L::kRows < H) ln.store(out + u * oh, Half<T>::pack(fa), Half<T>::pack(fb));
         }
       }
-      float c[kV], s[kV];
-      load_angles<T, D, kInter>(p, ln, b, n, c, s);
+    }
+    if (!wk.live()) break;
+  }
+}
+
+// Backward, walked the same way, with the next token's rows on their way while the current one's are
+// worked on; a warp keeps the weight gradient of its columns in registers, and a block adds its
+// warps' up in a fixed order into one partial row per side.
+template <typename T, int D, bool kInter, bool kFull, bool kMulti>
+__global__ void __launch_bounds__(kThreads, kBlocksBwd) qk_norm_rope_bwd_kernel(const Params p) {
+  using L = Lane<T, D, kInter, kFull>;
+  constexpr int kP = L::kP;
+  __shared__ float red[kWarps * L::kRows][D];
+  __shared__ int red_side[kWarps];
+  __shared__ volatile Strides st[2][3];  // of a side's x, dz and dx
+  if (threadIdx.x < 2) {
+    st[threadIdx.x][0].set(p.xs[threadIdx.x]);
+    st[threadIdx.x][1].set(p.ds[threadIdx.x]);
+    st[threadIdx.x][2].set(p.os[threadIdx.x]);
+  }
+  __syncthreads();
+  const L ln(p.rot);
+  Walk wk(p, kUnrollBwd * L::kRows, false);
+  const int warp = threadIdx.x >> 5, side = wk.kind;
+  const int h0 = wk.h0 + ln.row, H = p.H[side];
+  const T* x0 = static_cast<const T*>(p.x[side]) + ln.col;
+  const T* dz0 = static_cast<const T*>(p.dz[side]) + ln.col;
+  T* dx0 = static_cast<T*>(p.out[side]) + ln.col;
+  // a row past the last head is loaded as the last head's and neither written nor counted
+  long long xh[kUnrollBwd], dh[kUnrollBwd], oh[kUnrollBwd];
+  bool live[kUnrollBwd];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        float dy[kV], g[kV];
-        Vec<T>::unpack(rz[u], dy);
-        partners<T, kInter>(rz[u], ln.partner, g);
-        // the transpose turns the sine's sign
+  for (int u = 0; u < kUnrollBwd; ++u) {
+    const int h = min(h0 + u * L::kRows, H - 1);
+    live[u] = h0 + u * L::kRows < H;
+    xh[u] = h * p.xs[side].h;
+    dh[u] = h * p.ds[side].h;
+    oh[u] = h * p.os[side].h;
+  }
+  const T* w = static_cast<const T*>(p.w[side]);
+  float2 wa[kP], wb[kP], da[kP], db[kP];
+  ln.weights(w, wa, wb);
 #pragma unroll
-        for (int e = 0; e < kV; ++e)
-          dy[e] = ln.sign == 0 ? dy[e] : fmaf(-g[e], s[e], dy[e] * c[e]);
-        if (w != nullptr) {
-          float f[kV];
-          Vec<T>::unpack(rx[u], f);
-          float ss = 0.f, dot = 0.f;
+  for (int e = 0; e < kP; ++e) da[e] = db[e] = make_float2(0.f, 0.f);
+
+  struct Rows {
+    uint4 x[kUnrollBwd], z[kUnrollBwd];
+    Angles<T, D, kInter, kFull, kMulti> ang;
+    long long out;
+  };
+  Pos<kMulti> pos;
+  // start the loads of the walk's token and of the next one's position
+  auto fetch = [&](Rows& r) {
+    const T* x = x0 + st[side][0].at(wk.b, wk.n);
+    const T* dz = dz0 + st[side][1].at(wk.b, wk.n);
+    r.out = st[side][2].at(wk.b, wk.n);
 #pragma unroll
-          for (int e = 0; e < kV; ++e) {
-            ss = fmaf(f[e], f[e], ss);
-            dot = fmaf(dy[e] * wt[e], f[e], dot);
-          }
-          ss = row_sum<L::kLanes>(ss);
-          dot = row_sum<L::kLanes>(dot);
-          const float r = rsqrtf(ss * (1.f / D) + p.eps);
-          const float k = r * r * dot * (1.f / D);
-          // rows past the last head are zeros and add nothing (unless eps is 0, hence the test)
-          const bool live = h0 + u * L::kRows < H;
+    for (int u = 0; u < kUnrollBwd; ++u) {
+      r.z[u] = ln.load(dz + dh[u]);
+      if (w != nullptr) r.x[u] = ln.load(x + xh[u]);
+    }
+    r.ang.load(p, ln, pos);
+    wk.next(p);
+    if (wk.live()) pos.load(p, wk.b, wk.n);
+  };
+  auto work = [&](const Rows& r) {
+    T* dx = dx0 + r.out;
+    // dy: the transposed rotation turns the sine's sign
+    float2 ya[kUnrollBwd][kP], yb[kUnrollBwd][kP];
+    {
+      float2 ca[kP], sa[kP], cb[kP], sb[kP];
 #pragma unroll
-          for (int e = 0; e < kV; ++e) {
-            if (live) dw[e] = fmaf(dy[e] * r, f[e], dw[e]);
-            dy[e] = r * fmaf(-f[e], k, dy[e] * wt[e]);
-          }
-        }
-        const int h = h0 + u * L::kRows;
-        if (h < H) *reinterpret_cast<uint4*>(dx + h * os.h) = Vec<T>::pack(dy);
+      for (int e = 0; e < kP; ++e) {
+        ca[e] = r.ang.cosine(false, e);
+        cb[e] = r.ang.cosine(true, e);
+        const float2 s0 = r.ang.sine(false, e), s1 = r.ang.sine(true, e);
+        sa[e] = make_float2(-s0.x, -s0.y);
+        sb[e] = make_float2(-s1.x, -s1.y);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnrollBwd; ++u) {
+        Half<T>::unpack(r.z[u].x, r.z[u].y, ya[u]);
+        Half<T>::unpack(r.z[u].z, r.z[u].w, yb[u]);
+        turn<L, kInter, kFull>(ln, ya[u], yb[u], ca, sa, cb, sb);
       }
     }
     if (w != nullptr) {
+      float2 fa[kUnrollBwd][kP], fb[kUnrollBwd][kP];
+      float2 ga[kUnrollBwd][kP], gb[kUnrollBwd][kP];  // dy w
+      float sums[2 * kUnrollBwd];                     // of x^2 and of dy w x, per row
 #pragma unroll
-      for (int e = 0; e < kV; ++e) red[warp * L::kRows + ln.row][ln.col + e] = dw[e];
-      __syncthreads();
-      for (int i = threadIdx.x; i < D; i += kThreads) {
-        float t = 0.f;
+      for (int u = 0; u < kUnrollBwd; ++u) {
+        Half<T>::unpack(r.x[u].x, r.x[u].y, fa[u]);
+        Half<T>::unpack(r.x[u].z, r.x[u].w, fb[u]);
+        float2 ss = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < kWarps * L::kRows; ++k) t += red[k][i];
-        p.dw[(static_cast<size_t>(blockIdx.x) * 2 + side) * D + i] = t;
+        for (int e = 0; e < kP; ++e) {
+          ga[u][e] = mul2(ya[u][e], wa[e]);
+          gb[u][e] = mul2(yb[u][e], wb[e]);
+          ss = fma2(fa[u][e], fa[u][e], ss);
+          ss = fma2(fb[u][e], fb[u][e], ss);
+          dot = fma2(ga[u][e], fa[u][e], dot);
+          dot = fma2(gb[u][e], fb[u][e], dot);
+        }
+        sums[u] = ss.x + ss.y;
+        sums[kUnrollBwd + u] = dot.x + dot.y;
       }
-      __syncthreads();
+      static_assert(kUnrollBwd == 2, "four sums a step");
+      const float mine = sum4<L::kLanes>(sums[0], sums[1], sums[2], sums[3]);
+      const float r4 = rsqrtf(mine * (1.f / D) + p.eps);  // in the lanes that hold a sum of x^2
+#pragma unroll
+      for (int u = 0; u < kUnrollBwd; ++u) {
+        const float rn = from4<L::kLanes>(r4, u), dot = from4<L::kLanes>(mine, 2 + u);
+        const float k = -rn * rn * dot * (1.f / D);
+        const float2 rr = make_float2(rn, rn), kk = make_float2(k, k);
+        const float2 rl = live[u] ? rr : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < kP; ++e) {
+          da[e] = fma2(mul2(ya[u][e], rl), fa[u][e], da[e]);
+          db[e] = fma2(mul2(yb[u][e], rl), fb[u][e], db[e]);
+          ya[u][e] = mul2(rr, fma2(fa[u][e], kk, ga[u][e]));
+          yb[u][e] = mul2(rr, fma2(fb[u][e], kk, gb[u][e]));
+        }
+      }
     }
+#pragma unroll
+    for (int u = 0; u < kUnrollBwd; ++u)
+      if (live[u]) ln.store(dx + oh[u], Half<T>::pack(ya[u]), Half<T>::pack(yb[u]));
+  };
+  if (wk.live()) {
+    Rows even, odd;
+    pos.load(p, wk.b, wk.n);
+    fetch(even);
+    while (true) {
+      if (!wk.live()) {
+        work(even);
+        break;
+      }
+      fetch(odd);
+      work(even);
+      if (!wk.live()) {
+        work(odd);
+        break;
+      }
+      fetch(even);
+      work(odd);
+    }
+  }
+  if (p.dw == nullptr) return;
+#pragma unroll
+  for (int e = 0; e < kP; ++e) {
+    float* r = &red[warp * L::kRows + ln.row][ln.col + 2 * e];
+    r[0] = da[e].x, r[1] = da[e].y;
+    r[ln.gap] = db[e].x, r[ln.gap + 1] = db[e].y;
+  }
+  if ((threadIdx.x & 31) == 0) red_side[warp] = side;
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps * L::kRows; ++k)
+      if (red_side[k / L::kRows] == i / D) sum += red[k][i % D];
+    p.dw[static_cast<size_t>(blockIdx.x) * 2 * D + i] = sum;
   }
 }
 

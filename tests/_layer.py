@@ -105,9 +105,9 @@ def norm_rope_bwd(x, dz, w, rope, positions, sections=None, interleaved=False, e
 
 
 def dw_bound(mag_sum, rows):
-    """A weight gradient's terms have 14 roundings; a thread adds at most rows / (444 x 8) + 8 of
-    them in turn, its block 32 more, the last sum 14 + 32."""
-    return (14 + rows / 3552 + 8 + 32 + 46) * U * mag_sum
+    """A weight gradient's terms have 14 roundings; a thread adds at most rows / (296 blocks x 8
+    warps) + 8 of them in turn, its block 32 more, the last sum 10 + 32."""
+    return (14 + rows / 2368 + 8 + 32 + 42) * U * mag_sum
 
 
 def assert_within(got, ref, bound, dtype, what):
