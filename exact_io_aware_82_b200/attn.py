@@ -11,8 +11,10 @@ library is missing or no sm_100 device is present, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+import struct
 
 MASK_FULL, MASK_CAUSAL, MASK_SLIDING, MASK_LOCAL_GLOBAL = 0, 1, 2, 3
 ATTN_OK = 0
@@ -518,6 +520,85 @@ def attn_decode_noalloc(q, k, v, o=None, lse=None, scale=None, num_splits=0, ret
     return o, lse
 
 
+# ---- around attention ------------------------------------------------------------------------
+# A decode step makes several of these calls, so their checks spend little on arguments that are right.
+
+def _expect(t, name, dtype, shape):
+    """_check of one contiguous tensor of exactly this shape."""
+    import torch
+
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _check(t, name, dtype, len(shape), shape)
+
+
+def _expect_out(t, name, dtype, shape):
+    if t is not None:
+        _expect(t, name, dtype, shape)
+
+
+def _expect_view(t, name, dtype, shape, written=False):
+    """A strided tensor argument: type, dtype, shape and a contiguous last dimension; one that is
+    written must not hold an element twice (an expanded or self-overlapping view)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
+    if written and not t.is_contiguous():
+        end = 1
+        for step, n in sorted((t.stride(i), t.shape[i]) for i in range(t.dim()) if t.shape[i] > 1):
+            if step < end:
+                raise ValueError("%s overlaps itself: a tensor that is written needs rows of its own" % name)
+            end = step * (n - 1) + end
+
+
+def _one_device(stream, **tensors):
+    """The device of all tensors (and of the stream), as _device."""
+    index = -2
+    for t in tensors.values():
+        if t is not None:
+            i = t.get_device() if t.device.type == "cuda" else -1
+            if index == -2:
+                index = i
+            elif i != index:
+                index = -1
+    if index < 0 or stream is not None:
+        return _device(stream, **tensors)
+    return next(t.device for t in tensors.values() if t is not None)
+
+
+def _call(fn, where, dev, stream, *args):
+    """fn(*args, stream) with dev current; raises on a status."""
+    import torch
+
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, _raw_stream(dev.index, stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev.index, stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, where)
+
+
+def _raw_stream(index, stream):
+    import torch
+
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _at(t):
+    return t.data_ptr() if t is not None else None
+
+
+@functools.lru_cache(maxsize=1024)
 def attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len, max_seq_len,
                                               d) -> int:
     return int(lib().attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len,
@@ -542,67 +623,52 @@ def attn_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, gr
     num_pages, page_size, Hkv, dk = k_cache.shape
     if dk != d:
         raise ValueError("k_cache and v_cache must both be [num_pages, page_size, Hkv, d]")
-    _check(v_cache, "v_cache", torch.bfloat16, 4, k_cache.shape)
+    _expect(v_cache, "v_cache", torch.bfloat16, k_cache.shape)
     _check(prefix_table, "prefix_table", torch.int32, 2)
     num_groups = prefix_table.shape[0]
-    _check(prefix_lens, "prefix_lens", torch.int32, 1, (num_groups,))
-    _check(group_starts, "group_starts", torch.int32, 1, (num_groups + 1,))
+    _expect(prefix_lens, "prefix_lens", torch.int32, (num_groups,))
+    _expect(group_starts, "group_starts", torch.int32, (num_groups + 1,))
     _check(block_table, "block_table", torch.int32, 2)
     if block_table.shape[0] != B:
         raise ValueError("block_table and seq_lens need one row per sequence")
-    _check(seq_lens, "seq_lens", torch.int32, 1, (B,))
-    _check_out(o, "o", torch.bfloat16, (B, Hq, 1, d))
-    _check_out(lse, "lse", torch.float32, (B, Hq))
+    _expect(seq_lens, "seq_lens", torch.int32, (B,))
+    _expect_out(o, "o", torch.bfloat16, (B, Hq, 1, d))
+    _expect_out(lse, "lse", torch.float32, (B, Hq))
     _check_workspace(workspace, 0)
-    dev = _device(stream, q=q, k_cache=k_cache, v_cache=v_cache, prefix_table=prefix_table,
-                  prefix_lens=prefix_lens, group_starts=group_starts, block_table=block_table,
-                  seq_lens=seq_lens, o=o, lse=lse, workspace=workspace)
+    dev = _one_device(stream, q=q, k_cache=k_cache, v_cache=v_cache, prefix_table=prefix_table,
+                      prefix_lens=prefix_lens, group_starts=group_starts, block_table=block_table,
+                      seq_lens=seq_lens, o=o, lse=lse, workspace=workspace)
     max_prefix_len, max_seq_len = int(max_prefix_len), int(max_seq_len)
-    with torch.cuda.device(dev):
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None and return_lse:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-        if workspace is None:
-            nbytes = attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len,
-                                                               max_seq_len, d)
-            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-        rc = lib().attn_decode_shared_prefix(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(prefix_table),
-            _ptr(prefix_lens), _ptr(group_starts), _ptr(block_table), _ptr(seq_lens), B, Hq, Hkv,
-            num_groups, num_pages, page_size, prefix_table.shape[1], max_prefix_len,
-            block_table.shape[1], max_seq_len, d, scale, _ptr(workspace), workspace.numel(),
-            _stream_ptr(stream))
-    _raise(rc, "attn_decode_shared_prefix")
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None and return_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    if workspace is None:
+        nbytes = attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len,
+                                                           max_seq_len, d)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    _call(lib().attn_decode_shared_prefix, "attn_decode_shared_prefix", dev, stream, q.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), _at(lse), prefix_table.data_ptr(),
+          prefix_lens.data_ptr(), group_starts.data_ptr(), block_table.data_ptr(),
+          seq_lens.data_ptr(), B, Hq, Hkv, num_groups, num_pages, page_size, prefix_table.shape[1],
+          max_prefix_len, block_table.shape[1], max_seq_len, d,
+          1.0 / math.sqrt(d) if scale is None else float(scale), workspace.data_ptr(),
+          workspace.numel())
     return o, lse
-
-
-def _check_view(t, name, dtype, shape, written=False):
-    """A strided tensor argument: type, dtype, shape and a contiguous last dimension; one that is
-    written must not hold an element twice (an expanded or self-overlapping view)."""
-    import torch
-
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    if t.stride(-1) != 1:
-        raise ValueError("%s must be contiguous in its last dimension" % name)
-    if written and not t.is_contiguous():
-        end = 1
-        for step, n in sorted((t.stride(i), t.shape[i]) for i in range(t.dim()) if t.shape[i] > 1):
-            if step < end:
-                raise ValueError("%s overlaps itself: a tensor that is written needs rows of its own" % name)
-            end = step * (n - 1) + end
 
 
 def _bhn(t):
     """(b, h, n) element strides of a [B,H,N,d] or packed [T,H,d] tensor."""
     s = t.stride()
     return s[:3] if len(s) == 4 else (0, s[1], s[0])
+
+
+@functools.lru_cache(maxsize=64)
+def _section_array(sections, pairs):
+    if not 1 <= len(sections) <= 4 or min(sections) < 0 or sum(sections) != pairs:
+        raise ValueError("sections must be 1 to 4 counts of pairs that add up to rope.shape[1] / 2 = %d, got %s"
+                         % (pairs, list(sections)))
+    return (ctypes.c_int * len(sections))(*sections)
 
 
 class _QkShapes:
@@ -614,53 +680,58 @@ class _QkShapes:
 
         if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor):
             raise TypeError("q and k must be torch.Tensors")
-        if q.dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError("q must be torch.bfloat16 or torch.float32, got %s" % q.dtype)
-        if q.dim() not in (3, 4) or k.dim() != q.dim():
+        dtype = q.dtype
+        if dtype is not torch.bfloat16 and dtype is not torch.float32:
+            raise TypeError("q must be torch.bfloat16 or torch.float32, got %s" % dtype)
+        q_shape, k_shape = q.shape, k.shape
+        if len(q_shape) not in (3, 4) or len(k_shape) != len(q_shape):
             raise ValueError("q and k must both be [B, H, N, d] or both packed [tokens, H, d]")
-        self.dtype, self.code = q.dtype, 0 if q.dtype == torch.bfloat16 else 1
-        self.dense = q.dim() == 4
+        self.dtype, self.code = dtype, 0 if dtype is torch.bfloat16 else 1
+        self.dense = len(q_shape) == 4
         if self.dense:
-            self.B, self.Hq, self.N, self.d = q.shape
-            self.Hkv = k.shape[1]
+            B, Hq, N, d = q_shape
+            Hkv = k_shape[1]
+            k_want = (B, Hkv, N, d)
         else:
-            self.B, (self.N, self.Hq, self.d) = 1, q.shape
-            self.Hkv = k.shape[1]
-        self.q_shape, self.k_shape = self.shape(self.Hq), self.shape(self.Hkv)
-        _check_view(q, "q", self.dtype, self.q_shape)
-        _check_view(k, "k", self.dtype, self.k_shape)
-        for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if t is not None:
-                _check(t, n, self.dtype, 1, (self.d,))
+            B, (N, Hq, d) = 1, q_shape
+            Hkv = k_shape[1]
+            k_want = (N, Hkv, d)
+        self.q_shape, self.k_shape = q_shape, k_want
+        _expect_view(q, "q", dtype, q_shape)
+        _expect_view(k, "k", dtype, k_want)
+        if q_weight is not None:
+            _expect(q_weight, "q_weight", dtype, (d,))
+        if k_weight is not None:
+            _expect(k_weight, "k_weight", dtype, (d,))
         _check(rope, "rope", torch.float32, 2)
-        self.max_pos, self.rot = rope.shape
-        self.sections, self.axes = None, 1
+        max_pos, rot = rope.shape
+        axes = 1
+        self.sections = None
+        lead = ()
         if sections is not None:
-            sections = [int(x) for x in sections]
-            self.axes = len(sections)
-            if not 1 <= self.axes <= 4 or min(sections) < 0 or 2 * sum(sections) != self.rot:
-                raise ValueError("sections must be 1 to 4 counts of pairs that add up to rope.shape[1] / 2 = %d, got %s"
-                                 % (self.rot // 2, sections))
-            self.sections = (ctypes.c_int * self.axes)(*sections)
-        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
+            self.sections = _section_array(tuple(map(int, sections)), rot // 2)
+            axes = len(sections)
+            lead = (axes,)
+        if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32:
             raise TypeError("positions must be a torch.int32 tensor")
-        lead = () if sections is None else (self.axes,)
-        wants = [lead + (self.N,)] + ([lead + (self.B, self.N)] if self.dense else [])
-        if tuple(positions.shape) not in wants:
-            raise ValueError("positions must have shape %s, got %s"
-                             % (" or ".join(map(str, wants)), tuple(positions.shape)))
-        if self.N > 1 and positions.stride(-1) != 1:
+        shape = positions.shape
+        per_row = self.dense and shape == lead + (B, N)
+        if not per_row and shape != lead + (N,):
+            raise ValueError("positions must have shape %s%s, got %s" % (
+                lead + (N,), " or %s" % (lead + (B, N),) if self.dense else "", tuple(shape)))
+        if N > 1 and positions.stride(-1) != 1:
             raise ValueError("positions must be contiguous in its last dimension")
-        self.pos = (positions.stride(0) if lead else 0,
-                    positions.stride(-2) if positions.dim() == len(lead) + 2 else 0)
-
-    def shape(self, heads):
-        return (self.B, heads, self.N, self.d) if self.dense else (self.N, heads, self.d)
+        self.pos = (positions.stride(0) if lead else 0, positions.stride(-2) if per_row else 0)
+        self.N, self.Hq, self.Hkv, self.d = N, Hq, Hkv, d
+        # what the library is told: sizes, and from the head size on the rest
+        self.sizes = (B, N, Hq, Hkv)
+        self.rest = (d, rot, max_pos, axes)
 
 
 def _longs(*parts):
+    """A host array of long long."""
     flat = [x for p in parts for x in p]
-    return (ctypes.c_longlong * len(flat))(*flat)
+    return struct.pack("%dq" % len(flat), *flat)
 
 
 def attn_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, sections=None, interleaved=False,
@@ -681,25 +752,23 @@ def attn_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, sections=None, 
 
     s = _QkShapes(q, k, q_weight, k_weight, rope, positions, sections)
     if q_out is not None:
-        _check_view(q_out, "q_out", s.dtype, s.q_shape, written=True)
+        _expect_view(q_out, "q_out", s.dtype, s.q_shape, written=True)
     if k_out is not None:
-        _check_view(k_out, "k_out", s.dtype, s.k_shape, written=True)
-    dev = _device(stream, q=q, k=k, q_weight=q_weight, k_weight=k_weight, rope=rope,
-                  positions=positions, q_out=q_out, k_out=k_out)
-    with torch.cuda.device(dev):
-        if q_out is None:
-            q_out = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
-        if k_out is None:
-            k_out = torch.empty(s.k_shape, dtype=s.dtype, device=dev)
-        rc = lib().attn_qk_norm_rope(
-            _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(q_weight), _ptr(k_weight), _ptr(rope),
-            _ptr(positions), _longs(_bhn(q), _bhn(k), _bhn(q_out), _bhn(k_out), s.pos), s.sections,
-            s.code, s.B, s.N, s.Hq, s.Hkv, s.d, s.rot, s.max_pos, s.axes, int(interleaved),
-            float(eps), _stream_ptr(stream))
-    _raise(rc, "attn_qk_norm_rope")
+        _expect_view(k_out, "k_out", s.dtype, s.k_shape, written=True)
+    dev = _one_device(stream, q=q, k=k, q_weight=q_weight, k_weight=k_weight, rope=rope,
+                      positions=positions, q_out=q_out, k_out=k_out)
+    if q_out is None:
+        q_out = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
+    if k_out is None:
+        k_out = torch.empty(s.k_shape, dtype=s.dtype, device=dev)
+    _call(lib().attn_qk_norm_rope, "attn_qk_norm_rope", dev, stream, q.data_ptr(), k.data_ptr(),
+          q_out.data_ptr(), k_out.data_ptr(), _at(q_weight), _at(k_weight), rope.data_ptr(),
+          positions.data_ptr(), _longs(_bhn(q), _bhn(k), _bhn(q_out), _bhn(k_out), s.pos), s.sections,
+          s.code, *s.sizes, *s.rest, 1 if interleaved else 0, float(eps))
     return q_out, k_out
 
 
+@functools.lru_cache(maxsize=16)
 def attn_qk_norm_rope_bwd_workspace_bytes(d) -> int:
     return int(lib().attn_qk_norm_rope_bwd_workspace_bytes(d))
 
@@ -716,39 +785,38 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope, positi
     import torch
 
     s = _QkShapes(q, k, q_weight, k_weight, rope, positions, sections)
-    _check_view(dq_out, "dq_out", s.dtype, s.q_shape)
-    _check_view(dk_out, "dk_out", s.dtype, s.k_shape)
+    _expect_view(dq_out, "dq_out", s.dtype, s.q_shape)
+    _expect_view(dk_out, "dk_out", s.dtype, s.k_shape)
     if dq is not None:
-        _check_view(dq, "dq", s.dtype, s.q_shape, written=True)
+        _expect_view(dq, "dq", s.dtype, s.q_shape, written=True)
     if dk is not None:
-        _check_view(dk, "dk", s.dtype, s.k_shape, written=True)
+        _expect_view(dk, "dk", s.dtype, s.k_shape, written=True)
     for t, w, n in ((dq_weight, q_weight, "dq_weight"), (dk_weight, k_weight, "dk_weight")):
-        if t is not None and w is None:
-            raise ValueError("%s is given but the weight is not" % n)
-        _check_out(t, n, torch.float32, (s.d,))
+        if t is not None:
+            if w is None:
+                raise ValueError("%s is given but the weight is not" % n)
+            _expect(t, n, torch.float32, (s.d,))
     _check_workspace(workspace, 0)
-    dev = _device(stream, q=q, k=k, dq_out=dq_out, dk_out=dk_out, q_weight=q_weight, k_weight=k_weight,
-                  rope=rope, positions=positions, dq=dq, dk=dk, dq_weight=dq_weight,
-                  dk_weight=dk_weight, workspace=workspace)
-    with torch.cuda.device(dev):
-        if dq is None:
-            dq = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
-        if dk is None:
-            dk = torch.empty(s.k_shape, dtype=s.dtype, device=dev)
-        if dq_weight is None and q_weight is not None:
-            dq_weight = torch.empty(s.d, dtype=torch.float32, device=dev)
-        if dk_weight is None and k_weight is not None:
-            dk_weight = torch.empty(s.d, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(max(attn_qk_norm_rope_bwd_workspace_bytes(s.d), 16),
-                                    dtype=torch.uint8, device=dev)
-        rc = lib().attn_qk_norm_rope_bwd(
-            _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(q_weight),
-            _ptr(k_weight), _ptr(dq_weight), _ptr(dk_weight), _ptr(rope), _ptr(positions),
-            _longs(_bhn(q), _bhn(k), _bhn(dq_out), _bhn(dk_out), _bhn(dq), _bhn(dk), s.pos),
-            s.sections, s.code, s.B, s.N, s.Hq, s.Hkv, s.d, s.rot, s.max_pos, s.axes,
-            int(interleaved), float(eps), _ptr(workspace), workspace.numel(), _stream_ptr(stream))
-    _raise(rc, "attn_qk_norm_rope_bwd")
+    dev = _one_device(stream, q=q, k=k, dq_out=dq_out, dk_out=dk_out, q_weight=q_weight,
+                      k_weight=k_weight, rope=rope, positions=positions, dq=dq, dk=dk,
+                      dq_weight=dq_weight, dk_weight=dk_weight, workspace=workspace)
+    if dq is None:
+        dq = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
+    if dk is None:
+        dk = torch.empty(s.k_shape, dtype=s.dtype, device=dev)
+    if dq_weight is None and q_weight is not None:
+        dq_weight = torch.empty(s.d, dtype=torch.float32, device=dev)
+    if dk_weight is None and k_weight is not None:
+        dk_weight = torch.empty(s.d, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(attn_qk_norm_rope_bwd_workspace_bytes(s.d), 16),
+                                dtype=torch.uint8, device=dev)
+    _call(lib().attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd", dev, stream, q.data_ptr(), k.data_ptr(),
+          dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _at(q_weight),
+          _at(k_weight), _at(dq_weight), _at(dk_weight), rope.data_ptr(), positions.data_ptr(),
+          _longs(_bhn(q), _bhn(k), _bhn(dq_out), _bhn(dk_out), _bhn(dq), _bhn(dk), s.pos),
+          s.sections, s.code, *s.sizes, *s.rest, 1 if interleaved else 0, float(eps),
+          workspace.data_ptr(), workspace.numel())
     return dq, dk, dq_weight, dk_weight
 
 
@@ -763,28 +831,25 @@ def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, rope, positions, slots,
     import torch
 
     s = _QkShapes(q, k, q_weight, k_weight, rope, positions, sections)
-    if s.dense or s.dtype != torch.bfloat16:
+    if s.dense or s.code != 0:
         raise ValueError("q, k and v must be packed bf16 [tokens, H, d] tensors")
-    _check_view(v, "v", s.dtype, s.k_shape)
-    _check(slots, "slots", torch.int32, 1, (s.N,))
+    _expect_view(v, "v", s.dtype, s.k_shape)
+    _expect(slots, "slots", torch.int32, (s.N,))
     _check(k_cache, "k_cache", torch.bfloat16, 4)
     num_pages, page_size = k_cache.shape[:2]
-    _check(k_cache, "k_cache", torch.bfloat16, 4, (num_pages, page_size, s.Hkv, s.d))
-    _check(v_cache, "v_cache", torch.bfloat16, 4, k_cache.shape)
+    _expect(k_cache, "k_cache", torch.bfloat16, (num_pages, page_size, s.Hkv, s.d))
+    _expect(v_cache, "v_cache", torch.bfloat16, k_cache.shape)
     if q_out is not None:
-        _check_view(q_out, "q_out", s.dtype, s.q_shape, written=True)
-    dev = _device(stream, q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, rope=rope,
-                  positions=positions, slots=slots, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
-    with torch.cuda.device(dev):
-        if q_out is None:
-            q_out = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
-        rc = lib().attn_qk_norm_rope_paged(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(q_weight),
-            _ptr(k_weight), _ptr(rope), _ptr(positions), _ptr(slots),
-            _longs(_bhn(q), _bhn(k), _bhn(v), _bhn(q_out), s.pos[:1]), s.sections, s.N, s.Hq, s.Hkv,
-            num_pages, page_size, s.d, s.rot, s.max_pos, s.axes, int(interleaved), float(eps),
-            _stream_ptr(stream))
-    _raise(rc, "attn_qk_norm_rope_paged")
+        _expect_view(q_out, "q_out", s.dtype, s.q_shape, written=True)
+    dev = _one_device(stream, q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, rope=rope,
+                      positions=positions, slots=slots, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
+    if q_out is None:
+        q_out = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
+    _call(lib().attn_qk_norm_rope_paged, "attn_qk_norm_rope_paged", dev, stream, q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _at(q_weight),
+          _at(k_weight), rope.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+          _longs(_bhn(q), _bhn(k), _bhn(v), _bhn(q_out), s.pos[:1]), s.sections, s.N, s.Hq, s.Hkv,
+          num_pages, page_size, *s.rest, 1 if interleaved else 0, float(eps))
     return q_out
 
 
@@ -808,35 +873,33 @@ def attn_page_update(block_table, old_lens, new_lens, free_pages, ring, page_siz
 
     _check(block_table, "block_table", torch.int32, 2)
     B, max_pages = block_table.shape
-    _check(old_lens, "old_lens", torch.int32, 1, (B,))
-    _check(new_lens, "new_lens", torch.int32, 1, (B,))
+    _expect(old_lens, "old_lens", torch.int32, (B,))
+    _expect(new_lens, "new_lens", torch.int32, (B,))
     _check(free_pages, "free_pages", torch.int32, 1)
-    _check(ring, "ring", torch.int64, 1, (3,))
+    _expect(ring, "ring", torch.int64, (3,))
     max_tokens = int(max_tokens)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    _check_out(pos_offset, "pos_offset", torch.int32, (B,))
-    _check_out(ring_out, "ring_out", torch.int64, (3,))
-    _check_out(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
-    _check_out(slots, "slots", torch.int32, (max_tokens,))
-    _check_out(positions, "positions", torch.int32, (max_tokens,))
-    dev = _device(stream, block_table=block_table, old_lens=old_lens, new_lens=new_lens,
-                  free_pages=free_pages, ring=ring, pos_offset=pos_offset, ring_out=ring_out,
-                  cu_seqlens=cu_seqlens, slots=slots, positions=positions)
-    with torch.cuda.device(dev):
-        if ring_out is None:
-            ring_out = torch.empty(3, dtype=torch.int64, device=dev)
-        if cu_seqlens is None:
-            cu_seqlens = torch.empty(B + 1, dtype=torch.int32, device=dev)
-        if slots is None:
-            slots = torch.empty(max_tokens, dtype=torch.int32, device=dev)
-        if positions is None:
-            positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
-        rc = lib().attn_page_update(
-            _ptr(block_table), _ptr(old_lens), _ptr(new_lens), _ptr(free_pages), _ptr(ring),
-            _ptr(ring_out), _ptr(cu_seqlens), _ptr(slots), _ptr(positions), _ptr(pos_offset), B,
-            max_pages, int(page_size), free_pages.numel(), max_tokens, _stream_ptr(stream))
-    _raise(rc, "attn_page_update")
+    _expect_out(pos_offset, "pos_offset", torch.int32, (B,))
+    _expect_out(ring_out, "ring_out", torch.int64, (3,))
+    _expect_out(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    _expect_out(slots, "slots", torch.int32, (max_tokens,))
+    _expect_out(positions, "positions", torch.int32, (max_tokens,))
+    dev = _one_device(stream, block_table=block_table, old_lens=old_lens, new_lens=new_lens,
+                      free_pages=free_pages, ring=ring, pos_offset=pos_offset, ring_out=ring_out,
+                      cu_seqlens=cu_seqlens, slots=slots, positions=positions)
+    if ring_out is None:
+        ring_out = torch.empty(3, dtype=torch.int64, device=dev)
+    if cu_seqlens is None:
+        cu_seqlens = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    if slots is None:
+        slots = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+    if positions is None:
+        positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+    _call(lib().attn_page_update, "attn_page_update", dev, stream, block_table.data_ptr(),
+          old_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), ring.data_ptr(),
+          ring_out.data_ptr(), cu_seqlens.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+          _at(pos_offset), B, max_pages, int(page_size), free_pages.numel(), max_tokens)
     return ring_out, cu_seqlens, slots, positions
 
 

@@ -1193,30 +1193,33 @@ int log2_int(int x) {
 constexpr int kPfxCtas = 148;
 
 struct PfxLayout {
-  long long own_row0, rows;
+  long long thin_row0, own_row0, rows;
   size_t lse_offset, plan_offset, total;
 };
 
 PfxLayout pfx_layout(int B, int Hq, int Hkv, int num_groups) {
   PfxLayout L{};
   const int G = Hq / Hkv;
-  L.own_row0 = 2ll * B * Hq + static_cast<long long>(kPfxCtas) * pfx::kCtaRows;
+  L.thin_row0 = 2ll * B * Hq + static_cast<long long>(kPfxCtas) * pfx::kWideCtaRows;
+  L.own_row0 = L.thin_row0 + 2ll * B * Hq + static_cast<long long>(kPfxCtas) * pfx::kThinCtaRows;
   L.rows = L.own_row0 + 2ll * B * Hq + 2ll * G * kPfxCtas;
   L.lse_offset = static_cast<size_t>(L.rows) * pfx::kD * sizeof(float);
   L.plan_offset = (L.lse_offset + static_cast<size_t>(L.rows) * sizeof(float) + 15) & ~size_t(15);
-  L.total = L.plan_offset + (2 + static_cast<size_t>(num_groups) + B) * sizeof(int);
+  L.total = L.plan_offset + (4 + 2 * static_cast<size_t>(num_groups) + B) * sizeof(int);
   return L;
 }
 
-// Shapes that the prefix decode takes (the line of steps is counted in 32 bits).
+// Shapes that the prefix decode takes (the lines of steps are counted in 32 bits).
 int pfx_shapes(int B, int Hq, int Hkv, int num_groups, int max_prefix_len, int max_seq_len, int d) {
   if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || num_groups < 0 || max_prefix_len < 0 || max_seq_len < 0)
     return ATTN_ERR_INVALID_ARG;
   const int G = Hq / Hkv;
   if (d != pfx::kD || (G != 1 && G != 2 && G != 4 && G != 8)) return ATTN_ERR_UNSUPPORTED;
   const double blocks = std::min<double>(B, B / (256 / G) + static_cast<double>(num_groups));
-  const double cost = Hkv * (blocks * (max_prefix_len / 128 + 1.0) * pfx::kCostBoth + blocks * pfx::kCostJob +
-                             static_cast<double>(B) * ((max_seq_len / 128 + 1.0) * pfx::kCostAlt + pfx::kCostJob));
+  const double cost = Hkv * (blocks * ((max_prefix_len / 128 + 1.0) * pfx::kCostBoth + pfx::kCostWideJob) +
+                             static_cast<double>(B) * ((max_seq_len / 128 + 1.0) * pfx::kCostThinMax + pfx::kCostThinJob));
+  // grid (Hkv, B) of the joining kernel, and partial rows in 32 bits
+  if (B > 65535 || 6.0 * B * Hq + 148.0 * 512 > 2.0e9) return ATTN_ERR_UNSUPPORTED;
   return cost < 2.0e9 ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
 }
 
@@ -1248,6 +1251,38 @@ int encode_map_decode_q(CUtensorMap* map, const void* base, int heads, int B, in
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// Page pool [rows][heads][128], rows a multiple of 8, as (64 columns, 8 rows, 2 column halves, groups of 8
+// rows, heads), read as boxes of box_rows rows of one head, both halves (the tile layout of
+// decode_prefix.cuh).  A group index past the last reads as zero.
+int encode_map_pages(CUtensorMap* map, const void* base, int rows, int heads, uint32_t box_rows) {
+  const cuuint64_t row = static_cast<cuuint64_t>(heads) * pfx::kD * 2;
+  const cuuint64_t dims[5] = {64, 8, 2, static_cast<cuuint64_t>(rows) / 8, static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, static_cast<cuuint64_t>(pfx::kD) * 2};
+  const cuuint32_t box[5] = {64, 8, 2, box_rows / 8, 1};
+  const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims,
+                        strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// Launch with the next kernel of the stream allowed to start early: that kernel waits for this one's
+// results by itself (griddepcontrol.wait).
+template <typename... A>
+int launch_early(void (*kern)(A...), dim3 blocks, unsigned threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = blocks;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, args...));
 }
 
 }  // namespace
@@ -1525,6 +1560,7 @@ int attn_decode_shared_prefix(const void* q, const void* k_cache, const void* v_
   p.max_pages = max_pages_per_seq;
   p.num_pages = num_pages;
   p.page_shift = log2_int(page_size);
+  p.thin_cost = pfx::cost_thin_step(p.page_shift);
   p.prefix_table = prefix_table;
   p.prefix_lens = prefix_lens;
   p.group_starts = group_starts;
@@ -1536,26 +1572,29 @@ int attn_decode_shared_prefix(const void* q, const void* k_cache, const void* v_
   p.ws_o = static_cast<float*>(workspace);
   p.ws_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.lse_offset);
   p.plan = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + L.plan_offset);
+  p.thin_row0 = L.thin_row0;
   p.own_row0 = L.own_row0;
 
-  CUtensorMap tq, tq_own, tk, tv;
+  CUtensorMap tq, tq_thin, tq_own, tk, tv;
   const int rows = num_pages * page_size;
   const uint32_t piece = static_cast<uint32_t>(std::min(page_size, pfx::kTile));
   if (encode_map_decode_q(&tq, q, Hq, B, p.G, p.S) != ATTN_OK ||
+      encode_map_decode_q(&tq_thin, q, Hq, B, p.G, pfx::kThinRows / p.G) != ATTN_OK ||
       encode_map_decode_q(&tq_own, q, Hq, B, p.G, 1) != ATTN_OK ||
-      encode_map_packed(&tk, k_cache, rows, Hkv, piece) != ATTN_OK ||
-      encode_map_packed(&tv, v_cache, rows, Hkv, piece) != ATTN_OK)
+      encode_map_pages(&tk, k_cache, rows, Hkv, piece) != ATTN_OK ||
+      encode_map_pages(&tv, v_cache, rows, Hkv, piece) != ATTN_OK)
     return ATTN_ERR_UNSUPPORTED;
   const int ctas = std::min(info->num_sms, kPfxCtas);
   if (scale < 0.f)
-    pfx::decode_prefix_kernel<true><<<ctas, pfx::kThreads, pfx::kSmemBytes, st>>>(tq, tq_own, tk, tv, p);
+    pfx::decode_prefix_kernel<true><<<ctas, pfx::kThreads, pfx::kSmemBytes, st>>>(tq, tq_thin, tq_own, tk, tv, p);
   else
-    pfx::decode_prefix_kernel<false><<<ctas, pfx::kThreads, pfx::kSmemBytes, st>>>(tq, tq_own, tk, tv, p);
+    pfx::decode_prefix_kernel<false><<<ctas, pfx::kThreads, pfx::kSmemBytes, st>>>(tq, tq_thin, tq_own, tk, tv, p);
   if ((rc = cuda_status(cudaGetLastError())) != ATTN_OK) return rc;
-  const long long rows_out = static_cast<long long>(B) * Hq;
-  pfx::decode_prefix_combine_kernel<<<static_cast<unsigned>((rows_out + pfx::kCombineWarps - 1) / pfx::kCombineWarps),
-                                      pfx::kCombineWarps * 32, 0, st>>>(p, static_cast<__nv_bfloat16*>(o), lse);
-  return cuda_status(cudaGetLastError());
+  void (*combine)(pfx::Params, __nv_bfloat16*, float*) =
+      p.G == 1 ? pfx::decode_prefix_combine_kernel<1> : p.G == 2 ? pfx::decode_prefix_combine_kernel<2>
+      : p.G == 4 ? pfx::decode_prefix_combine_kernel<4> : pfx::decode_prefix_combine_kernel<8>;
+  return launch_early<pfx::Params, __nv_bfloat16*, float*>(combine, dim3(Hkv, B), std::max(32 * p.G, 128), st, p,
+                                                           static_cast<__nv_bfloat16*>(o), lse);
 }
 
 }  // extern "C"

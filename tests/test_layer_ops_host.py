@@ -111,9 +111,10 @@ def test_shared_prefix_refusals(lib):
     assert prefix(lib, B_=100000, Hq=64, Hkv=64, ml=1 << 20, mp=1 << 16) == U
     need = A.attn_decode_shared_prefix_workspace_bytes
     assert need(2, 8, 3, 1, 64, 64, 128) == 0 and need(2, 8, 2, 1, 64, 64, 64) == 0 and need(-1, 8, 2, 1, 64, 64, 128) == 0
-    # partial rows: 2 B Hq for the prefixes and for the own keys, 256 and 2 G more for each of 148 CTAs
-    rows = 4 * 64 * 32 + 148 * (256 + 8)
-    assert need(64, 32, 8, 3, 5000, 100, 128) == -(-rows * 516 // 16) * 16 + 4 * (2 + 3 + 64)
+    # partial rows: 2 B Hq for wide and for thin prefix parts and for the own keys, and 256, 32 and 2 G
+    # more for each of 148 CTAs; the plan
+    rows = 6 * 64 * 32 + 148 * (256 + 32 + 8)
+    assert need(64, 32, 8, 3, 5000, 100, 128) == -(-rows * 516 // 16) * 16 + 4 * (4 + 2 * 3 + 64)
 
 
 def t(*shape, dtype=bf16, device="cpu"):
