@@ -559,17 +559,15 @@ def _expect_view(t, name, dtype, shape, written=False):
 
 def _one_device(stream, **tensors):
     """The device of all tensors (and of the stream), as _device."""
-    index = -2
+    index = None
     for t in tensors.values():
         if t is not None:
-            i = t.get_device() if t.device.type == "cuda" else -1
-            if index == -2:
-                index = i
-            elif i != index:
-                index = -1
-    if index < 0 or stream is not None:
-        return _device(stream, **tensors)
-    return next(t.device for t in tensors.values() if t is not None)
+            i = t.get_device()  # -1 where it is not a CUDA tensor
+            if i != index:
+                if index is not None or i < 0:
+                    return _device(stream, **tensors)  # refuses them
+                index, first = i, t
+    return first.device if stream is None else _device(stream, **tensors)
 
 
 def _call(fn, where, dev, stream, *args):

@@ -13,9 +13,10 @@
 //
 // Bound by latency: a step of 64 requests moves a few KB.  So it is one launch without any
 // communication between blocks: every block sums all requests for itself (three sums in one scan,
-// the results kept in shared memory) and then takes its share of the rows and of the tokens; a
-// token that falls into a page taken in this very step reads it from the ring, not from the
-// table row another block is writing.
+// the results kept in shared memory) and then takes its share of the pages moved and of the
+// tokens, a thread each, whatever request they belong to (an ended request returns thousands of
+// pages); a token that falls into a page taken in this very step reads it from the ring, not from
+// the table row another block is writing.
 #pragma once
 
 #include <cstdint>
@@ -59,7 +60,11 @@ __global__ void __launch_bounds__(kThreads) page_update_kernel(const Params p) {
   __shared__ Sums warp_sums[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long max_len = static_cast<long long>(p.max_pages) << p.page_shift;
+  const long long head = p.ring_in[0], tail = p.ring_in[1], held = tail - head;
 
+  // the ring's ends as places in it
+  const int head0 = p.cap > 0 && head > 0 ? static_cast<int>(static_cast<unsigned long long>(head) % p.cap) : 0;
+  const int tail0 = p.cap > 0 && tail > 0 ? static_cast<int>(static_cast<unsigned long long>(tail) % p.cap) : 0;
   // each thread sums a run of requests, the block scans the threads' sums
   const int per = (p.B + kThreads - 1) / kThreads;
   const int first = min(tid * per, p.B), last = min(first + per, p.B);
@@ -91,7 +96,6 @@ __global__ void __launch_bounds__(kThreads) page_update_kernel(const Params p) {
     if (w < warp) before.grow += s.grow, before.shrink += s.shrink, before.tokens += s.tokens;
     all.grow += s.grow, all.shrink += s.shrink, all.tokens += s.tokens;
   }
-  const long long head = p.ring_in[0], tail = p.ring_in[1], held = tail - head;
   bad = bad || head < 0 || held < 0 || held > p.cap || held + all.shrink > p.cap ||
         all.tokens > p.max_tokens;
   const long long missing = bad ? -1 : max(all.grow - held, 0ll);
@@ -124,31 +128,36 @@ __global__ void __launch_bounds__(kThreads) page_update_kernel(const Params p) {
   __syncthreads();
   for (int b = gtid; b <= p.B; b += threads) p.cu[b] = cu[b];
 
-  const int head0 = static_cast<int>(p.cap > 0 ? head % p.cap : 0);
-  const int tail0 = static_cast<int>(p.cap > 0 ? tail % p.cap : 0);
   // entry `at` places behind `from` in the ring (both below cap)
   auto ring = [&](int from, int at) {
     const long long i = static_cast<long long>(from) + at;
     return static_cast<int>(i >= p.cap ? i - p.cap : i);
   };
-  // block table rows: a warp per request
-  for (int b = blockIdx.x * kWarps + warp; b < p.B; b += gridDim.x * kWarps) {
-    const int had = pages_of(__ldg(p.old_lens + b), p.page_shift);
-    const int need = pages_of(__ldg(p.new_lens + b), p.page_shift);
-    int* row = p.table + static_cast<size_t>(b) * p.max_pages;
-    for (int j = lane; j < need - had; j += 32) row[had + j] = p.free_pages[ring(head0, grow0[b] + j)];
-    for (int j = lane; j < had - need; j += 32) p.free_pages[ring(tail0, shrink0[b] + j)] = row[need + j];
+  // the last request whose sum is not above x
+  auto find = [&](const int* sums, int x) {
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int m = (lo + hi) >> 1;
+      if (sums[m] <= x) lo = m;
+      else hi = m;
+    }
+    return lo;
+  };
+  // pages taken, then pages returned: a thread per page
+  const int taken = static_cast<int>(all.grow), returned = static_cast<int>(all.shrink);
+  for (int m = gtid; m < taken; m += threads) {
+    const int b = find(grow0, m), had = pages_of(__ldg(p.old_lens + b), p.page_shift);
+    p.table[static_cast<size_t>(b) * p.max_pages + had + (m - grow0[b])] = p.free_pages[ring(head0, m)];
+  }
+  for (int m = gtid; m < returned; m += threads) {
+    const int b = find(shrink0, m), need = pages_of(__ldg(p.new_lens + b), p.page_shift);
+    p.free_pages[ring(tail0, m)] = p.table[static_cast<size_t>(b) * p.max_pages + need + (m - shrink0[b])];
   }
   // tokens: a thread per token
   for (int t = gtid; t < p.max_tokens; t += threads) {
     int slot = -1, pos = 0;
     if (t < cu[p.B]) {
-      int lo = 0, hi = p.B;  // the last request with cu[lo] <= t
-      while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (cu[m] <= t) lo = m;
-        else hi = m;
-      }
+      const int lo = find(cu, t);
       const int a = __ldg(p.old_lens + lo), at = a + (t - cu[lo]);
       const int had = pages_of(a, p.page_shift), i = at >> p.page_shift;
       const int page = i < had ? p.table[static_cast<size_t>(lo) * p.max_pages + i]
