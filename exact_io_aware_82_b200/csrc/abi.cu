@@ -1135,50 +1135,75 @@ int qkn_common(qkn::Params& p, const void* q_weight, const void* k_weight, const
   return ATTN_OK;
 }
 
-// Warps of a norm + rotation call: every item (a warp's heads of one token) of its own, up to a grid of
-// per_sm blocks per SM (what its registers allow), and at least one warp for every group of heads.
-int qkn_blocks(const qkn::Params& p, int d, int size, int unroll, bool paged, int grid, long long* blocks) {
-  const int heads = unroll * (512 / (d * size));
-  const long long chunks = (p.H[0] + heads - 1) / heads +
-                           static_cast<long long>(paged ? 2 : 1) * ((p.H[1] + heads - 1) / heads);
-  const long long want = (static_cast<long long>(p.B) * p.N * chunks + qkn::kWarps - 1) / qkn::kWarps;
-  const long long least = (chunks + qkn::kWarps - 1) / qkn::kWarps;
-  *blocks = std::max(std::min<long long>(want, grid), least);
-  return *blocks <= (1 << 20) ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+// One token of a [B][H][1][d] call per batch row: the same as one row of B tokens, which fills tiles.
+void qkn_flatten(qkn::Params& p, long long* st, int views, const long long* strides) {
+  std::copy(strides, strides + 3 * views + 2, st);
+  p.pos_axis = st[3 * views];
+  p.pos_b = st[3 * views + 1];
+  if (p.N != 1 || p.B <= 1 || p.pos_b != 1) return;
+  for (int v = 0; v < views; ++v) st[3 * v + 2] = st[3 * v];
+  p.N = p.B;
+  p.B = 1;
 }
 
-template <bool kPaged>
-int launch_qkn(const qkn::Params& p, int dtype, int d, bool inter, int num_sms, cudaStream_t st) {
-  long long blocks = 0;
-  int rc = qkn_blocks(p, d, dtype == ATTN_DTYPE_BF16 ? 2 : 4, qkn::kUnroll, kPaged, qkn::kBlocks * num_sms, &blocks);
-  if (rc != ATTN_OK) return rc;
-  void (*kern)(const qkn::Params) = nullptr;
-  using bf16 = __nv_bfloat16;
-  const bool full = p.rot == d, multi = p.axes > 1;
-#define ATTN_QKN_PICK(T, D)                                                                             \
-  kern = full ? (multi ? (inter ? qkn::qk_norm_rope_kernel<T, D, true, true, true, kPaged>                \
-                                : qkn::qk_norm_rope_kernel<T, D, false, true, true, kPaged>)              \
-                       : (inter ? qkn::qk_norm_rope_kernel<T, D, true, true, false, kPaged>               \
-                                : qkn::qk_norm_rope_kernel<T, D, false, true, false, kPaged>))            \
-              : (multi ? (inter ? qkn::qk_norm_rope_kernel<T, D, true, false, true, kPaged>               \
-                                : qkn::qk_norm_rope_kernel<T, D, false, false, true, kPaged>)             \
-                       : (inter ? qkn::qk_norm_rope_kernel<T, D, true, false, false, kPaged>              \
-                                : qkn::qk_norm_rope_kernel<T, D, false, false, false, kPaged>))
-  if constexpr (kPaged) {
-    ATTN_QKN_PICK(bf16, 128);
-  } else {
-    if (dtype == ATTN_DTYPE_BF16 && d == 128) ATTN_QKN_PICK(bf16, 128);
-    else if (dtype == ATTN_DTYPE_BF16) ATTN_QKN_PICK(bf16, 64);
-    else if (d == 128) ATTN_QKN_PICK(float, 128);
-    else ATTN_QKN_PICK(float, 64);
-  }
-#undef ATTN_QKN_PICK
-  kern<<<static_cast<unsigned>(blocks), qkn::kThreads, 0, st>>>(p);
-  return cuda_status(cudaGetLastError());
+// [B][H][N][d] view as (d, H, N, B), in tiles of kTokens tokens x `heads` heads.
+int encode_map_heads(CUtensorMap* map, const void* base, const long long* st, int B, int H, int N, int d,
+                     int dtype, int heads) {
+  const int size = dtype == ATTN_DTYPE_BF16 ? 2 : 4;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(N),
+                              static_cast<cuuint64_t>(B)};
+  // the stride of a dimension of one entry does not count (and may be anything)
+  const cuuint64_t strides[3] = {H > 1 ? static_cast<cuuint64_t>(st[1]) * size : 16u,
+                                 N > 1 ? static_cast<cuuint64_t>(st[2]) * size : 16u,
+                                 B > 1 ? static_cast<cuuint64_t>(st[0]) * size : 16u};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(heads), qkn::kTokens, 1};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, dtype == ATTN_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                        4, const_cast<void*>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
 }
 
-// blocks of the backward pass, and rows of its partial weight gradients
-constexpr int kQknBwdBlocks = 148 * qkn::kBlocksBwd;
+// Blocks of a tiled call: a whole number for each group of heads (a block's tiles all have the same heads),
+// every tile of its own up to `most` blocks.
+int qkn_tile_blocks(const qkn::Params& p, int heads, int most, int* chunks, int* cq, unsigned* blocks) {
+  *cq = (p.H[0] + heads - 1) / heads;
+  const long long ch = *cq + static_cast<long long>((p.H[1] + heads - 1) / heads);
+  if (ch > most) return ATTN_ERR_UNSUPPORTED;  // more groups of heads than blocks
+  const long long runs = static_cast<long long>(p.B) * ((p.N + qkn::kTokens - 1) / qkn::kTokens);
+  *chunks = static_cast<int>(ch);
+  *blocks = static_cast<unsigned>(ch * std::min<long long>(runs, most / ch));
+  return ATTN_OK;
+}
+
+constexpr int kQknBwdBlocks = 148 * qkn::kTileBlocksBwd;  // and rows of partial weight gradients
+
+// kernel KERNEL<type, d, interleaved, rot_dim == d, several axes> for a call
+#define ATTN_QKN_PICK_D(KERNEL, T, D)                                                        \
+  (full ? (multi ? (inter ? KERNEL<T, D, true, true, true> : KERNEL<T, D, false, true, true>)  \
+                 : (inter ? KERNEL<T, D, true, true, false> : KERNEL<T, D, false, true, false>)) \
+        : (multi ? (inter ? KERNEL<T, D, true, false, true> : KERNEL<T, D, false, false, true>)  \
+                 : (inter ? KERNEL<T, D, true, false, false> : KERNEL<T, D, false, false, false>)))
+#define ATTN_QKN_PICK(KERNEL)                                                                \
+  (dtype == ATTN_DTYPE_BF16                                                                  \
+       ? (d == 128 ? ATTN_QKN_PICK_D(KERNEL, __nv_bfloat16, 128) : ATTN_QKN_PICK_D(KERNEL, __nv_bfloat16, 64)) \
+       : (d == 128 ? ATTN_QKN_PICK_D(KERNEL, float, 128) : ATTN_QKN_PICK_D(KERNEL, float, 64)))
+
+// Launch with the next kernel of the stream allowed to start early: that kernel waits for this one's
+// results by itself (griddepcontrol.wait).
+template <typename... A>
+int launch_early(void (*kern)(A...), dim3 blocks, unsigned threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = blocks;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, args...));
+}
 
 bool page_size_ok(int page_size) {
   return page_size >= 8 && page_size <= (1 << 20) && (page_size & (page_size - 1)) == 0;
@@ -1269,22 +1294,6 @@ int encode_map_pages(CUtensorMap* map, const void* base, int rows, int heads, ui
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// Launch with the next kernel of the stream allowed to start early: that kernel waits for this one's
-// results by itself (griddepcontrol.wait).
-template <typename... A>
-int launch_early(void (*kern)(A...), dim3 blocks, unsigned threads, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = blocks;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kern, args...));
-}
-
 }  // namespace
 }  // namespace attn
 
@@ -1310,22 +1319,27 @@ int attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, co
   DeviceInfo* info = nullptr;
   if ((rc = current_device(&info)) != ATTN_OK) return rc;
   if (empty) return ATTN_OK;
-  p.x[0] = q;
-  p.x[1] = k;
-  p.out[0] = q_out;
-  p.out[1] = k_out;
-  p.xs[0] = make_view(strides);
-  p.xs[1] = make_view(strides + 3);
-  p.os[0] = make_view(strides + 6);
-  p.os[1] = make_view(strides + 9);
-  p.pos_axis = strides[12];
-  p.pos_b = strides[13];
-  return launch_qkn<false>(p, dtype, d, interleaved != 0, info->num_sms,
-                           reinterpret_cast<cudaStream_t>(stream));
+  if ((rc = configure_fwd(info)) != ATTN_OK) return rc;  // the tensor-map encoder
+  long long st[14];
+  qkn_flatten(p, st, 4, strides);
+  const int heads = qkn::kUnroll * (512 / (d * size));
+  int chunks = 0, cq = 0;
+  unsigned blocks = 0;
+  if ((rc = qkn_tile_blocks(p, heads, qkn::kTileBlocks * info->num_sms, &chunks, &cq, &blocks)) != ATTN_OK) return rc;
+  CUtensorMap tq, tk, tqo, tko;
+  if ((rc = encode_map_heads(&tq, q, st, p.B, Hq, p.N, d, dtype, heads)) != ATTN_OK ||
+      (rc = encode_map_heads(&tk, k, st + 3, p.B, Hkv, p.N, d, dtype, heads)) != ATTN_OK ||
+      (rc = encode_map_heads(&tqo, q_out, st + 6, p.B, Hq, p.N, d, dtype, heads)) != ATTN_OK ||
+      (rc = encode_map_heads(&tko, k_out, st + 9, p.B, Hkv, p.N, d, dtype, heads)) != ATTN_OK)
+    return rc;
+  const bool full = rot_dim == d, multi = num_axes > 1, inter = interleaved != 0;
+  auto* kern = ATTN_QKN_PICK(qkn::qk_norm_rope_kernel);
+  kern<<<blocks, qkn::kTileThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(tq, tk, tqo, tko, p);
+  return cuda_status(cudaGetLastError());
 }
 
 size_t attn_qk_norm_rope_bwd_workspace_bytes(int d) {
-  return d == 64 || d == 128 ? static_cast<size_t>(kQknBwdBlocks) * 2 * d * sizeof(float) : 0;
+  return d == 64 || d == 128 ? static_cast<size_t>(kQknBwdBlocks) * d * sizeof(float) : 0;
 }
 
 int attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
@@ -1361,53 +1375,37 @@ int attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, cons
   if (weighted && (workspace == nullptr || !aligned16(workspace) ||
                    workspace_bytes < attn_qk_norm_rope_bwd_workspace_bytes(d)))
     return ATTN_ERR_WORKSPACE;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  int blocks = 0;
+  cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+  int chunks = 1, cq = 0;
+  unsigned blocks = 0;
   if (!empty) {
-    p.x[0] = q;
-    p.x[1] = k;
-    p.dz[0] = dq_out;
-    p.dz[1] = dk_out;
-    p.out[0] = dq;
-    p.out[1] = dk;
-    p.xs[0] = make_view(strides);
-    p.xs[1] = make_view(strides + 3);
-    p.ds[0] = make_view(strides + 6);
-    p.ds[1] = make_view(strides + 9);
-    p.os[0] = make_view(strides + 12);
-    p.os[1] = make_view(strides + 15);
-    p.pos_axis = strides[18];
-    p.pos_b = strides[19];
+    if ((rc = configure_fwd(info)) != ATTN_OK) return rc;  // the tensor-map encoder
+    long long st[20];
+    qkn_flatten(p, st, 6, strides);
     p.dw = weighted ? static_cast<float*>(workspace) : nullptr;
-    long long want = 0;
-    if ((rc = qkn_blocks(p, d, size, qkn::kUnrollBwd, false, kQknBwdBlocks, &want)) != ATTN_OK) return rc;
-    if (want > kQknBwdBlocks) return ATTN_ERR_UNSUPPORTED;  // more heads than the partial rows' warps
-    blocks = static_cast<int>(want);
-    using bf16 = __nv_bfloat16;
-    void (*kern)(const qkn::Params) = nullptr;
+    const int heads = qkn::kUnrollBwd * (512 / (d * size));
+    if ((rc = qkn_tile_blocks(p, heads, std::min(qkn::kTileBlocksBwd * info->num_sms, kQknBwdBlocks), &chunks, &cq,
+                              &blocks)) != ATTN_OK)
+      return rc;
+    CUtensorMap t[6];
+    const void* views[6] = {q, k, dq_out, dk_out, dq, dk};
+    for (int i = 0; i < 6; ++i) {
+      if ((i == 0 && q_weight == nullptr) || (i == 1 && k_weight == nullptr)) {
+        t[i] = CUtensorMap{};  // not read
+        continue;
+      }
+      if ((rc = encode_map_heads(&t[i], views[i], st + 3 * i, p.B, i % 2 ? Hkv : Hq, p.N, d, dtype, heads)) != ATTN_OK)
+        return rc;
+    }
     const bool full = rot_dim == d, multi = num_axes > 1, inter = interleaved != 0;
-#define ATTN_QKN_PICK(T, D)                                                                             \
-  kern = full ? (multi ? (inter ? qkn::qk_norm_rope_bwd_kernel<T, D, true, true, true>                    \
-                                : qkn::qk_norm_rope_bwd_kernel<T, D, false, true, true>)                  \
-                       : (inter ? qkn::qk_norm_rope_bwd_kernel<T, D, true, true, false>                   \
-                                : qkn::qk_norm_rope_bwd_kernel<T, D, false, true, false>))                \
-              : (multi ? (inter ? qkn::qk_norm_rope_bwd_kernel<T, D, true, false, true>                   \
-                                : qkn::qk_norm_rope_bwd_kernel<T, D, false, false, true>)                 \
-                       : (inter ? qkn::qk_norm_rope_bwd_kernel<T, D, true, false, false>                  \
-                                : qkn::qk_norm_rope_bwd_kernel<T, D, false, false, false>))
-    if (dtype == ATTN_DTYPE_BF16 && d == 128) ATTN_QKN_PICK(bf16, 128);
-    else if (dtype == ATTN_DTYPE_BF16) ATTN_QKN_PICK(bf16, 64);
-    else if (d == 128) ATTN_QKN_PICK(float, 128);
-    else ATTN_QKN_PICK(float, 64);
-#undef ATTN_QKN_PICK
-    kern<<<static_cast<unsigned>(blocks), qkn::kThreads, 0, st>>>(p);
+    auto* kern = ATTN_QKN_PICK(qkn::qk_norm_rope_bwd_kernel);
+    kern<<<blocks, qkn::kTileThreads, 0, strm>>>(t[0], t[1], t[2], t[3], t[4], t[5], p);
     if ((rc = cuda_status(cudaGetLastError())) != ATTN_OK) return rc;
   }
-  if (weighted) {
-    qkn::qk_norm_dw_kernel<<<dim3(d / 32, 2), 1024, 0, st>>>(static_cast<const float*>(workspace),
-                                                             blocks, d, dq_weight, dk_weight);
-    rc = cuda_status(cudaGetLastError());
-  }
+  if (weighted)
+    rc = launch_early<const float*, int, int, int, int, float*, float*>(
+        qkn::qk_norm_dw_kernel, dim3(d / 8, 2), 8 * qkn::kSumRows, strm, static_cast<const float*>(workspace),
+        static_cast<int>(blocks), chunks, cq, d, dq_weight, dk_weight);
   return rc;
 }
 
@@ -1448,8 +1446,16 @@ int attn_qk_norm_rope_paged(const void* q, const void* k, const void* v, void* q
   p.cache[0] = k_cache;
   p.cache[1] = v_cache;
   p.slots_total = num_pages * page_size;
-  return launch_qkn<true>(p, ATTN_DTYPE_BF16, d, interleaved != 0, info->num_sms,
-                           reinterpret_cast<cudaStream_t>(stream));
+  // a warp per item (its heads of one token) up to kBlocks blocks per SM, one at least for every group of heads
+  const int heads = qkn::kUnroll * 2;
+  const long long chunks = (Hq + heads - 1) / heads + 2ll * ((Hkv + heads - 1) / heads);
+  const long long want = (T * chunks + qkn::kWarps - 1) / qkn::kWarps, least = (chunks + qkn::kWarps - 1) / qkn::kWarps;
+  const long long blocks = std::max(std::min<long long>(want, qkn::kBlocks * info->num_sms), least);
+  if (blocks > (1 << 20)) return ATTN_ERR_UNSUPPORTED;
+  const bool full = rot_dim == d, multi = num_axes > 1, inter = interleaved != 0;
+  auto* kern = ATTN_QKN_PICK_D(qkn::qk_norm_rope_paged_kernel, __nv_bfloat16, 128);
+  kern<<<static_cast<unsigned>(blocks), qkn::kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return cuda_status(cudaGetLastError());
 }
 
 int attn_page_update(int* block_table, const int* old_lens, const int* new_lens, int* free_pages,

@@ -17,28 +17,29 @@
 // the memory's rate is its instructions, and the layout of a row over lanes follows from that:
 //   - a lane holds 16 bytes of a row as two halves A and B: kH columns and their kH partners (i and
 //     i + rot_dim / 2), or 2 kH adjacent columns when interleaved, so a pair never leaves its lane;
-//   - a warp takes the same heads of every step-th token: weights stay in registers, the token's
-//     table columns are loaded once for kUnroll row loads, addresses advance by additions;
-//   - the kUnroll row sums are reduced together (each step of the exchange halves the values a lane
-//     still carries), so r is computed once per row instead of once per lane and row;
+//   - a warp takes the same heads of many tokens: weights stay in registers, the token's table
+//     columns are loaded once for all of its row loads;
+//   - the row sums of an item are reduced together (each step of the exchange halves the values a
+//     lane still carries), so r is computed once per row instead of once per lane and row;
 //   - arithmetic is in pairs of fp32 values.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <cstdint>
 
 #include "common.cuh"
+#include "dev/ptx_store.cuh"
 
 namespace attn {
 namespace qkn {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of the paged form
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;     // row loads of a warp's item, forward
 constexpr int kUnrollBwd = 2;  // backward: of x and of dz
-constexpr int kBlocks = 3;     // per SM, forward: 80 registers a thread
-constexpr int kBlocksBwd = 2;  // per SM, backward
+constexpr int kBlocks = 3;     // per SM, paged form: 80 registers a thread
 constexpr int kMaxAxes = 4;
 
 // Element strides of a [B][H][N][d] view (d contiguous).
@@ -47,11 +48,7 @@ struct View {
 };
 
 struct Params {
-  const void* x[2];   // queries, keys
-  void* out[2];       // forward: z; backward: dx
-  const void* dz[2];  // backward
-  const void* w[2];   // weights [d], or null: not normalised
-  View xs[2], os[2], ds[2];
+  const void* w[2];   // weights of queries and keys [d], or null: not normalised
   const float* rope;  // [max_pos][rot]: cosines, then sines
   const int* pos;     // [axes][B][N] by the strides below
   long long pos_axis, pos_b;
@@ -59,10 +56,12 @@ struct Params {
   int axes, rot, max_pos;
   int B, N, H[2];
   float eps;
-  float* dw;  // backward: partial weight gradients [blocks][2][d]
-  // paged form: the values, and tokens with a negative slot are left out
+  float* dw;  // backward: partial weight gradients [blocks][d], or null
+  // paged form: queries and keys, where the queries go, the values; tokens with a negative slot are left out
+  const void* x[2];
+  void* out[1];
   const void* v;
-  View vs;
+  View xs[2], os[1], vs;
   const int* slots;
   void* cache[2];
   int slots_total;
@@ -132,6 +131,20 @@ struct Lane {
                    : "=r"(r.z), "=r"(r.w) : "l"(p + gap) : "memory");
     }
     return r;
+  }
+  // this lane's halves of a row load that lies in shared memory as it does in memory
+  __device__ __forceinline__ uint4 read(const uint8_t* rows) const {
+    const uint8_t* p = rows + row * (D * sizeof(T)) + col * sizeof(T);
+    if constexpr (kInter) {
+      return *reinterpret_cast<const uint4*>(p);
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      const uint2 y = *reinterpret_cast<const uint2*>(p + gap * sizeof(T));
+      return make_uint4(x.x, x.y, y.x, y.y);
+    }
+  }
+  __device__ __forceinline__ void write(uint8_t* rows, uint2 a, uint2 b) const {
+    store(reinterpret_cast<T*>(rows + row * (D * sizeof(T)) + col * sizeof(T)), a, b);
   }
   __device__ __forceinline__ void store(T* p, uint2 a, uint2 b) const {
     if constexpr (kInter) {
@@ -289,103 +302,115 @@ __device__ __forceinline__ float from4(float x, int i) {
   return __shfl_sync(0xffffffffu, x, base + (i >> 1) * (kLanes / 2) + (i & 1) * (kLanes / 4));
 }
 
-// Which heads and tokens a warp takes: the same heads (queries, keys or values) of every step-th
-// token, with the token's place (b, n) and its offsets kept up by additions.
-struct Walk {
-  int kind, h0, left;    // left: tokens from the current one to the end
-  int step, step_b, step_n;
-  int b, n;
-  __device__ __forceinline__ Walk(const Params& p, int heads, bool paged) {
-    const int cq = (p.H[0] + heads - 1) / heads, ck = (p.H[1] + heads - 1) / heads;
-    const int chunks = cq + (paged ? 2 : 1) * ck;
-    const int warps = gridDim.x * kWarps, w = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    step = warps / chunks;  // the launch has chunks warps at least
-    const int token = w / chunks, chunk = w % chunks;
-    left = token < step ? p.B * p.N - token : 0;
-    kind = chunk < cq ? 0 : chunk < cq + ck ? 1 : 2;
-    h0 = (chunk - (kind == 0 ? 0 : kind == 1 ? cq : cq + ck)) * heads;
-    b = token / p.N;
-    n = token % p.N;
-    step_b = step / p.N;
-    step_n = step % p.N;
+// r = 1 / sqrt(mean(x^2) + eps) of the kUnroll rows in raw, in the lanes where sum4 leaves a row's sum.
+template <typename T, typename L>
+__device__ __forceinline__ float inverse_norms(const uint4 (&raw)[kUnroll], float eps) {
+  constexpr int kP = L::kP;
+  float ss[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    float2 fa[kP], fb[kP];
+    Half<T>::unpack(raw[u].x, raw[u].y, fa);
+    Half<T>::unpack(raw[u].z, raw[u].w, fb);
+    float2 t = mul2(fa[0], fa[0]);
+#pragma unroll
+    for (int e = 1; e < kP; ++e) t = fma2(fa[e], fa[e], t);
+#pragma unroll
+    for (int e = 0; e < kP; ++e) t = fma2(fb[e], fb[e], t);
+    ss[u] = t.x + t.y;
   }
-  __device__ __forceinline__ bool live() const { return left > 0; }
-  __device__ __forceinline__ void next(const Params& p) {
-    left -= step;
-    b += step_b;
-    n += step_n;
-    if (n >= p.N) {
-      n -= p.N;
-      ++b;
+  static_assert(kUnroll == 4, "four sums a step");
+  return rsqrtf(sum4<L::kLanes>(ss[0], ss[1], ss[2], ss[3]) * (1.f / (L::kLanes * 2 * L::kH)) + eps);
+}
+
+// Angle times weight, of the lane's columns and for their partners.
+template <typename L, bool kInter>
+struct Coeffs {
+  static constexpr int kP = L::kP;
+  float2 ca[kP], sa[kP], cb[kP], sb[kP];
+  template <typename A>
+  __device__ __forceinline__ Coeffs(const A& ang, const float2 (&wa)[kP], const float2 (&wb)[kP]) {
+#pragma unroll
+    for (int e = 0; e < kP; ++e) {
+      ca[e] = mul2(wa[e], ang.cosine(false, e));
+      cb[e] = mul2(wb[e], ang.cosine(true, e));
+      sa[e] = mul2(kInter ? swap2(wa[e]) : wb[e], ang.sine(false, e));
+      sb[e] = mul2(kInter ? swap2(wb[e]) : wa[e], ang.sine(true, e));
     }
   }
 };
 
+// ------------------------------------------------------------------------------------------
+// Paged form: rows by ordinary loads, because tokens are left out and go to scattered rows
+// ------------------------------------------------------------------------------------------
 // Strides that every token needs again: kept in shared memory and read there each time, so that they
-// do not hold registers through the loop (the loops below run at 80 registers, three blocks per SM).
+// do not hold registers through the loop (which runs at 80 registers, three blocks per SM).
 struct Strides {
-  long long b, n;
-  __device__ __forceinline__ void set(const View& v) volatile { b = v.b, n = v.n; }
-  __device__ __forceinline__ long long at(int ib, int in) const volatile { return ib * b + in * n; }
+  long long n;
+  __device__ __forceinline__ void set(const View& v) volatile { n = v.n; }
+  __device__ __forceinline__ long long at(int in) const volatile { return in * n; }
 };
 
-// Forward.
-template <typename T, int D, bool kInter, bool kFull, bool kMulti, bool kPaged>
-__global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_kernel(const Params p) {
+// bf16, packed tokens (B = 1).  A warp takes the same heads (queries, keys or values) of every step-th
+// token; the next token's position and slot are on their way while it works on the current one.
+template <typename T, int D, bool kInter, bool kFull, bool kMulti>
+__global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_paged_kernel(const Params p) {
   using L = Lane<T, D, kInter, kFull>;
   constexpr int kP = L::kP;
-  __shared__ volatile Strides st[3][2];  // of a kind's input and output
+  __shared__ volatile Strides st[4];  // of a kind's input, of the queries' output
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) st[i][0].set(p.xs[i]), st[i][1].set(p.os[i]);
-    st[2][0].set(p.vs);
+    for (int i = 0; i < 2; ++i) st[i].set(p.xs[i]);
+    st[2].set(p.vs);
+    st[3].set(p.os[0]);
   }
   __syncthreads();
   const L ln(p.rot);
-  Walk wk(p, kUnroll * L::kRows, kPaged);
-  if (!wk.live()) return;
-  const int side = wk.kind == 0 ? 0 : 1;
-  const bool copy = kPaged && wk.kind == 2;      // values: as they are
-  const bool to_cache = kPaged && wk.kind != 0;
-  const int h0 = wk.h0 + ln.row, H = p.H[side];
+  constexpr int kHeads = kUnroll * L::kRows;
+  const int cq = (p.H[0] + kHeads - 1) / kHeads, ck = (p.H[1] + kHeads - 1) / kHeads, chunks = cq + 2 * ck;
+  const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int step = gridDim.x * kWarps / chunks;  // the launch has chunks warps at least
+  const int chunk = warp % chunks;
+  int n = warp / chunks;
+  if (n >= step || n >= p.N) return;
+  const int kind = chunk < cq ? 0 : chunk < cq + ck ? 1 : 2, side = kind == 0 ? 0 : 1;
+  const bool copy = kind == 2;  // values: as they are
+  const int h0 = (chunk - (kind == 0 ? 0 : kind == 1 ? cq : cq + ck)) * kHeads + ln.row, H = p.H[side];
   const View& xs = copy ? p.vs : p.xs[side];
-  const View& os = p.os[side];
   const T* x0 = static_cast<const T*>(copy ? p.v : p.x[side]) + h0 * xs.h + ln.col;
-  T* out0 = to_cache ? static_cast<T*>(p.cache[wk.kind - 1]) + h0 * D + ln.col
-                     : static_cast<T*>(p.out[side]) + h0 * os.h + ln.col;
-  const long long xh = xs.h * L::kRows, oh = (to_cache ? D : os.h) * L::kRows;
+  T* out0 = kind != 0 ? static_cast<T*>(p.cache[kind - 1]) + h0 * D + ln.col
+                      : static_cast<T*>(p.out[0]) + h0 * p.os[0].h + ln.col;
+  const long long xh = xs.h * L::kRows, oh = (kind != 0 ? D : p.os[0].h) * L::kRows;
   const T* w = copy ? nullptr : static_cast<const T*>(p.w[side]);
   float2 wa[kP], wb[kP];
   ln.weights(w, wa, wb);
-  // the cache slot of the walk's token (below 0: left out)
-  auto slot_of = [&](const Walk& k) -> int {
-    if (!kPaged) return 0;
-    const int s = __ldg(p.slots + k.n);
+  // the cache slot of a token (below 0: left out)
+  auto slot_of = [&](int t) -> int {
+    const int s = __ldg(p.slots + t);
     if (s < p.slots_total) return s;
     atomicExch(&g_device_error, ATTN_ERR_INVALID_ARG);
     return -1;
   };
   Pos<kMulti> pos;
-  if (!copy) pos.load(p, wk.b, wk.n);
-  int slot = slot_of(wk);
+  if (!copy) pos.load(p, 0, n);
+  int slot = slot_of(n);
   while (true) {
-    const int b = wk.b, n = wk.n, cur = slot;
+    const int cur = slot, cn = n;
     const Pos<kMulti> cur_pos = pos;
-    wk.next(p);
-    const bool on = !kPaged || cur >= 0;
+    const bool more = p.N - n > step;
+    n += step;
     uint4 raw[kUnroll];
-    if (on) {
-      const T* x = x0 + st[wk.kind][0].at(b, n);
+    if (cur >= 0) {
+      const T* x = x0 + st[kind].at(cn);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
         raw[u] = h0 + u * L::kRows < H ? ln.load(x + u * xh) : make_uint4(0u, 0u, 0u, 0u);
     }
-    // the next token's position and slot are on their way meanwhile
-    if (wk.live()) {
-      if (!copy) pos.load(p, wk.b, wk.n);
-      slot = slot_of(wk);
+    if (more) {
+      if (!copy) pos.load(p, 0, n);
+      slot = slot_of(n);
     }
-    if (on) {
-      T* out = to_cache ? out0 + static_cast<long long>(cur) * p.H[1] * D : out0 + st[wk.kind][1].at(b, n);
+    if (cur >= 0) {
+      T* out = kind != 0 ? out0 + static_cast<long long>(cur) * p.H[1] * D : out0 + st[3].at(cn);
       if (copy) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
@@ -394,32 +419,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_kernel(const P
       } else {
         Angles<T, D, kInter, kFull, kMulti> ang;
         ang.load(p, ln, cur_pos);
-        // angle times weight: the column's own, and the partner's
-        float2 ca[kP], sa[kP], cb[kP], sb[kP];
-#pragma unroll
-        for (int e = 0; e < kP; ++e) {
-          ca[e] = mul2(wa[e], ang.cosine(false, e));
-          cb[e] = mul2(wb[e], ang.cosine(true, e));
-          sa[e] = mul2(kInter ? swap2(wa[e]) : wb[e], ang.sine(false, e));
-          sb[e] = mul2(kInter ? swap2(wb[e]) : wa[e], ang.sine(true, e));
-        }
-        float r4 = 1.f;
-        if (w != nullptr) {
-          float ss[kUnroll];
-#pragma unroll
-          for (int u = 0; u < kUnroll; ++u) {
-            float2 fa[kP], fb[kP];
-            Half<T>::unpack(raw[u].x, raw[u].y, fa);
-            Half<T>::unpack(raw[u].z, raw[u].w, fb);
-            float2 t = mul2(fa[0], fa[0]);
-#pragma unroll
-            for (int e = 1; e < kP; ++e) t = fma2(fa[e], fa[e], t);
-#pragma unroll
-            for (int e = 0; e < kP; ++e) t = fma2(fb[e], fb[e], t);
-            ss[u] = t.x + t.y;
-          }
-          r4 = rsqrtf(sum4<L::kLanes>(ss[0], ss[1], ss[2], ss[3]) * (1.f / D) + p.eps);
-        }
+        const Coeffs<L, kInter> k(ang, wa, wb);
+        const float r4 = w != nullptr ? inverse_norms<T, L>(raw, p.eps) : 1.f;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           const float r = from4<L::kLanes>(r4, u);
@@ -427,196 +428,344 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_kernel(const P
           float2 fa[kP], fb[kP];
           Half<T>::unpack(raw[u].x, raw[u].y, fa);
           Half<T>::unpack(raw[u].z, raw[u].w, fb);
-          turn<L, kInter, kFull>(ln, fa, fb, ca, sa, cb, sb);
+          turn<L, kInter, kFull>(ln, fa, fb, k.ca, k.sa, k.cb, k.sb);
 #pragma unroll
           for (int e = 0; e < kP; ++e) fa[e] = mul2(fa[e], rr), fb[e] = mul2(fb[e], rr);
           if (h0 + u * L::kRows < H) ln.store(out + u * oh, Half<T>::pack(fa), Half<T>::pack(fb));
         }
       }
     }
-    if (!wk.live()) break;
+    if (!more) break;
   }
 }
 
-// Backward, walked the same way, with the next token's rows on their way while the current one's are
-// worked on; a warp keeps the weight gradient of its columns in registers, and a block adds its
-// warps' up in a fixed order into one partial row per side.
-template <typename T, int D, bool kInter, bool kFull, bool kMulti>
-__global__ void __launch_bounds__(kThreads, kBlocksBwd) qk_norm_rope_bwd_kernel(const Params p) {
-  using L = Lane<T, D, kInter, kFull>;
-  constexpr int kP = L::kP;
-  __shared__ float red[kWarps * L::kRows][D];
-  __shared__ int red_side[kWarps];
-  __shared__ volatile Strides st[2][3];  // of a side's x, dz and dx
-  if (threadIdx.x < 2) {
-    st[threadIdx.x][0].set(p.xs[threadIdx.x]);
-    st[threadIdx.x][1].set(p.ds[threadIdx.x]);
-    st[threadIdx.x][2].set(p.os[threadIdx.x]);
+// ------------------------------------------------------------------------------------------
+// Dense and packed form, and the gradient: tiles of kTokens tokens x a few heads by TMA
+// ------------------------------------------------------------------------------------------
+// A block of four warps streams tiles through a ring in shared memory: one thread starts the load of
+// the tile after next, each warp works on one token of the current tile in place, and the result
+// leaves from the same buffer by one TMA store.  The tensor maps carry all strides (those of a fused
+// projection, of head-major or token-major outputs, 0 for broadcast heads), and clip heads and
+// tokens past the last.  So a thread holds no addresses and fits 72 registers: 28 warps per SM with
+// two tiles a block on their way.  A block's tiles all have the same heads.
+constexpr int kTokens = 4;
+constexpr int kTileThreads = 32 * kTokens;
+constexpr int kTileBlocks = 7;     // per SM: 72 registers a thread
+constexpr int kTileBlocksBwd = 6;  // backward: 80
+constexpr int kStages = 3;
+constexpr int kWarpBytes = 2048;  // of a stage: a warp's rows (backward: half of them x, half dz)
+constexpr int kStageBytes = kTokens * kWarpBytes;
+
+struct __align__(128) TileSmem {
+  uint8_t stage[kStages][kStageBytes];
+  uint64_t full[kStages];
+  int abort;
+};
+
+__device__ __forceinline__ void tile_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int h, int n, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(h), "r"(n), "r"(b)
+      : "memory");
+}
+__device__ __forceinline__ void tile_store(const CUtensorMap* map, uint32_t src, int h, int n, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(0), "r"(h), "r"(n), "r"(b)
+      : "memory");
+}
+
+// The tiles of a block: the same heads, every step-th run of kTokens tokens.
+struct Tiles {
+  int side, h0;   // queries or keys, first head
+  int left;       // runs from the current one to the end
+  int step, step_b, step_r, runs;
+  int b, r;       // batch row and run of the current tile
+  __device__ __forceinline__ Tiles(const Params& p, int heads) {
+    const int cq = (p.H[0] + heads - 1) / heads, chunks = cq + (p.H[1] + heads - 1) / heads;
+    const int chunk = blockIdx.x % chunks, first = blockIdx.x / chunks;
+    side = chunk < cq ? 0 : 1;
+    h0 = (chunk - (side ? cq : 0)) * heads;
+    step = gridDim.x / chunks;  // a whole number: the launch sees to it
+    runs = (p.N + kTokens - 1) / kTokens;
+    left = p.B * runs - first;
+    b = first / runs;
+    r = first % runs;
+    step_b = step / runs;
+    step_r = step % runs;
+  }
+  __device__ __forceinline__ bool live() const { return left > 0; }
+  __device__ __forceinline__ int n() const { return r * kTokens; }
+  __device__ __forceinline__ void next() {
+    left -= step;
+    b += step_b;
+    r += step_r;
+    if (r >= runs) {
+      r -= runs;
+      ++b;
+    }
+  }
+};
+
+// What both kernels do around a tile's arithmetic.  kInputs tensors of kBytes each per stage; the result
+// replaces the last of them.
+template <typename Work>
+__device__ __forceinline__ void stream_tiles(TileSmem& sm, Tiles tl, const CUtensorMap* in0, const CUtensorMap* in1,
+                                             const CUtensorMap* out, uint32_t bytes, Work&& work) {
+  const uint32_t base = dev::smem_u32(sm.stage[0]);
+  volatile int* abort = &sm.abort;
+  // start the load of tile number j of the block
+  auto load = [&](int j, const Tiles& t) {
+    if (!t.live()) return;
+    const int s = j % kStages;
+    const uint32_t bar = dev::smem_u32(&sm.full[s]), dst = base + s * kStageBytes;
+    dev::mbar_arrive_expect_tx(bar, in1 != nullptr ? 2 * bytes : bytes);
+    tile_load(dst, in0, bar, t.h0, t.n(), t.b);
+    if (in1 != nullptr) tile_load(dst + bytes, in1, bar, t.h0, t.n(), t.b);
+  };
+  if (threadIdx.x == 0) {
+    Tiles t = tl;
+    load(0, t);
+    t.next();
+    load(1, t);
+  }
+  const uint32_t from = in1 != nullptr ? bytes : 0;
+  bool ok = true;
+  int i = 0;
+  for (; tl.live(); ++i, tl.next()) {
+    const int s = i % kStages;
+    ok = work(sm.stage[s], tl, [&] { return wait_bounded(dev::smem_u32(&sm.full[s]), (i / kStages) & 1, abort); });
+    dev::fence_proxy_async_smem();
+    ok = __syncthreads_and(ok) != 0;
+    if (!ok) break;
+    if (threadIdx.x == 0) {
+      tile_store(out, base + s * kStageBytes + from, tl.h0, tl.n(), tl.b);
+      dev::bulk_commit_group();
+      dev::bulk_wait_group_read1();  // the tile before has left its stage: the one after next may come
+      Tiles t = tl;
+      t.next();
+      t.next();
+      load(i + 2, t);
+    }
+  }
+  if (threadIdx.x == 0) {
+    dev::bulk_wait_group_read0();
+    if (!ok) {  // a wait gave up: the tiles i and i + 1 may still be landing
+      wait_drain(dev::smem_u32(&sm.full[i % kStages]), (i / kStages) & 1);
+      tl.next();
+      if (tl.live()) wait_drain(dev::smem_u32(&sm.full[(i + 1) % kStages]), ((i + 1) / kStages) & 1);
+    }
+  }
+}
+
+__device__ __forceinline__ void init_tiles(TileSmem& sm) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) dev::mbar_init(dev::smem_u32(&sm.full[s]), 1);
+    sm.abort = 0;
+    dev::fence_barrier_init();
   }
   __syncthreads();
+}
+
+// Forward.
+template <typename T, int D, bool kInter, bool kFull, bool kMulti>
+__global__ void __launch_bounds__(kTileThreads, kTileBlocks)
+    qk_norm_rope_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_qo, const __grid_constant__ CUtensorMap tm_ko,
+                        const Params p) {
+  using L = Lane<T, D, kInter, kFull>;
+  constexpr int kP = L::kP;
+  __shared__ TileSmem sm;
+  init_tiles(sm);
   const L ln(p.rot);
-  Walk wk(p, kUnrollBwd * L::kRows, false);
-  const int warp = threadIdx.x >> 5, side = wk.kind;
-  const int h0 = wk.h0 + ln.row, H = p.H[side];
-  const T* x0 = static_cast<const T*>(p.x[side]) + ln.col;
-  const T* dz0 = static_cast<const T*>(p.dz[side]) + ln.col;
-  T* dx0 = static_cast<T*>(p.out[side]) + ln.col;
-  // a row past the last head is loaded as the last head's and neither written nor counted
-  long long xh[kUnrollBwd], dh[kUnrollBwd], oh[kUnrollBwd];
-  bool live[kUnrollBwd];
+  const Tiles tl(p, kUnroll * L::kRows);
+  const int warp = threadIdx.x >> 5;
+  const T* w = static_cast<const T*>(p.w[tl.side]);
+  float2 wa[kP], wb[kP];
+  ln.weights(w, wa, wb);
+  stream_tiles(sm, tl, tl.side ? &tm_k : &tm_q, nullptr, tl.side ? &tm_ko : &tm_qo, kStageBytes,
+               [&](uint8_t* stage, const Tiles& t, auto&& wait) {
+                 const int n = t.n() + warp;
+                 uint8_t* rows = stage + warp * kWarpBytes;
+                 Angles<T, D, kInter, kFull, kMulti> ang;
+                 if (n < p.N) {
+                   Pos<kMulti> pos;
+                   pos.load(p, t.b, n);
+                   ang.load(p, ln, pos);
+                 }
+                 if (!wait()) return false;
+                 if (n < p.N) {
+                   const Coeffs<L, kInter> k(ang, wa, wb);
+                   uint4 raw[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnrollBwd; ++u) {
-    const int h = min(h0 + u * L::kRows, H - 1);
-    live[u] = h0 + u * L::kRows < H;
-    xh[u] = h * p.xs[side].h;
-    dh[u] = h * p.ds[side].h;
-    oh[u] = h * p.os[side].h;
-  }
-  const T* w = static_cast<const T*>(p.w[side]);
+                   for (int u = 0; u < kUnroll; ++u) raw[u] = ln.read(rows + u * 512);
+                   const float r4 = w != nullptr ? inverse_norms<T, L>(raw, p.eps) : 1.f;
+#pragma unroll
+                   for (int u = 0; u < kUnroll; ++u) {
+                     const float r = from4<L::kLanes>(r4, u);
+                     const float2 rr = make_float2(r, r);
+                     float2 fa[kP], fb[kP];
+                     Half<T>::unpack(raw[u].x, raw[u].y, fa);
+                     Half<T>::unpack(raw[u].z, raw[u].w, fb);
+                     turn<L, kInter, kFull>(ln, fa, fb, k.ca, k.sa, k.cb, k.sb);
+#pragma unroll
+                     for (int e = 0; e < kP; ++e) fa[e] = mul2(fa[e], rr), fb[e] = mul2(fb[e], rr);
+                     ln.write(rows + u * 512, Half<T>::pack(fa), Half<T>::pack(fb));
+                   }
+                 }
+                 return true;
+               });
+}
+
+// Backward: the tile's x and dz, dx in place of dz; a warp keeps the weight gradient of its columns in
+// registers, and a block adds its warps' up in a fixed order into one partial row.
+template <typename T, int D, bool kInter, bool kFull, bool kMulti>
+__global__ void __launch_bounds__(kTileThreads, kTileBlocksBwd)
+    qk_norm_rope_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_gq, const __grid_constant__ CUtensorMap tm_gk,
+                            const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_dk,
+                            const Params p) {
+  using L = Lane<T, D, kInter, kFull>;
+  constexpr int kP = L::kP;
+  __shared__ TileSmem sm;
+  init_tiles(sm);
+  const L ln(p.rot);
+  const Tiles tl(p, kUnrollBwd * L::kRows);
+  const int warp = threadIdx.x >> 5;
+  const T* w = static_cast<const T*>(p.w[tl.side]);
+  const bool weighted = w != nullptr;
   float2 wa[kP], wb[kP], da[kP], db[kP];
   ln.weights(w, wa, wb);
 #pragma unroll
   for (int e = 0; e < kP; ++e) da[e] = db[e] = make_float2(0.f, 0.f);
-
-  struct Rows {
-    uint4 x[kUnrollBwd], z[kUnrollBwd];
-    Angles<T, D, kInter, kFull, kMulti> ang;
-    long long out;
-  };
-  Pos<kMulti> pos;
-  // start the loads of the walk's token and of the next one's position
-  auto fetch = [&](Rows& r) {
-    const T* x = x0 + st[side][0].at(wk.b, wk.n);
-    const T* dz = dz0 + st[side][1].at(wk.b, wk.n);
-    r.out = st[side][2].at(wk.b, wk.n);
+  const CUtensorMap* mx = tl.side ? &tm_k : &tm_q;
+  const CUtensorMap* mz = tl.side ? &tm_gk : &tm_gq;
+  stream_tiles(sm, tl, weighted ? mx : mz, weighted ? mz : nullptr, tl.side ? &tm_dk : &tm_dq, kStageBytes / 2,
+               [&](uint8_t* stage, const Tiles& t, auto&& wait) {
+                 const int n = t.n() + warp;
+                 const uint8_t* xrows = stage + warp * (kWarpBytes / 2);
+                 uint8_t* zrows = stage + (weighted ? kStageBytes / 2 : 0) + warp * (kWarpBytes / 2);
+                 Angles<T, D, kInter, kFull, kMulti> ang;
+                 if (n < p.N) {
+                   Pos<kMulti> pos;
+                   pos.load(p, t.b, n);
+                   ang.load(p, ln, pos);
+                 }
+                 if (!wait()) return false;
+                 if (n >= p.N) return true;
+                 // dy: the transposed rotation turns the sine's sign
+                 float2 ya[kUnrollBwd][kP], yb[kUnrollBwd][kP];
+                 {
+                   float2 ca[kP], sa[kP], cb[kP], sb[kP];
 #pragma unroll
-    for (int u = 0; u < kUnrollBwd; ++u) {
-      r.z[u] = ln.load(dz + dh[u]);
-      if (w != nullptr) r.x[u] = ln.load(x + xh[u]);
+                   for (int e = 0; e < kP; ++e) {
+                     ca[e] = ang.cosine(false, e);
+                     cb[e] = ang.cosine(true, e);
+                     const float2 s0 = ang.sine(false, e), s1 = ang.sine(true, e);
+                     sa[e] = make_float2(-s0.x, -s0.y);
+                     sb[e] = make_float2(-s1.x, -s1.y);
+                   }
+#pragma unroll
+                   for (int u = 0; u < kUnrollBwd; ++u) {
+                     const uint4 raw = ln.read(zrows + u * 512);
+                     Half<T>::unpack(raw.x, raw.y, ya[u]);
+                     Half<T>::unpack(raw.z, raw.w, yb[u]);
+                     turn<L, kInter, kFull>(ln, ya[u], yb[u], ca, sa, cb, sb);
+                   }
+                 }
+                 if (weighted) {
+                   uint4 raw[kUnrollBwd];
+                   float sums[2 * kUnrollBwd];  // of x^2 and of dy w x, per row
+#pragma unroll
+                   for (int u = 0; u < kUnrollBwd; ++u) {
+                     raw[u] = ln.read(xrows + u * 512);
+                     float2 fa[kP], fb[kP];
+                     Half<T>::unpack(raw[u].x, raw[u].y, fa);
+                     Half<T>::unpack(raw[u].z, raw[u].w, fb);
+                     float2 ss = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
+#pragma unroll
+                     for (int e = 0; e < kP; ++e) {
+                       ss = fma2(fa[e], fa[e], ss);
+                       ss = fma2(fb[e], fb[e], ss);
+                       dot = fma2(mul2(ya[u][e], wa[e]), fa[e], dot);
+                       dot = fma2(mul2(yb[u][e], wb[e]), fb[e], dot);
+                     }
+                     sums[u] = ss.x + ss.y;
+                     sums[kUnrollBwd + u] = dot.x + dot.y;
+                   }
+                   static_assert(kUnrollBwd == 2, "four sums a step");
+                   const float mine = sum4<L::kLanes>(sums[0], sums[1], sums[2], sums[3]);
+                   const float r4 = rsqrtf(mine * (1.f / D) + p.eps);  // in the lanes that hold a sum of x^2
+                   const int heads = p.H[tl.side] - tl.h0 - ln.row;
+#pragma unroll
+                   for (int u = 0; u < kUnrollBwd; ++u) {
+                     const float r = from4<L::kLanes>(r4, u), dot = from4<L::kLanes>(mine, 2 + u);
+                     const float k = -r * r * dot * (1.f / D);
+                     const float2 rr = make_float2(r, r), kk = make_float2(k, k);
+                     float2 fa[kP], fb[kP];
+                     Half<T>::unpack(raw[u].x, raw[u].y, fa);
+                     Half<T>::unpack(raw[u].z, raw[u].w, fb);
+                     // rows past the last head are zeros and add nothing (0 x infinity for eps = 0: hence rl)
+                     const float2 rl = u * L::kRows < heads ? rr : make_float2(0.f, 0.f);
+#pragma unroll
+                     for (int e = 0; e < kP; ++e) {
+                       da[e] = fma2(mul2(ya[u][e], rl), fa[e], da[e]);
+                       db[e] = fma2(mul2(yb[u][e], rl), fb[e], db[e]);
+                       ya[u][e] = mul2(rr, fma2(fa[e], kk, mul2(ya[u][e], wa[e])));
+                       yb[u][e] = mul2(rr, fma2(fb[e], kk, mul2(yb[u][e], wb[e])));
+                     }
+                   }
+                 }
+#pragma unroll
+                 for (int u = 0; u < kUnrollBwd; ++u)
+                   ln.write(zrows + u * 512, Half<T>::pack(ya[u]), Half<T>::pack(yb[u]));
+                 return true;
+               });
+  if (p.dw != nullptr) {
+    // the ring becomes the block's buffer of column sums [kTokens * kRows][D]
+    static_assert(kTokens * L::kRows * D * sizeof(float) <= sizeof(sm.stage), "column sums");
+    __syncthreads();
+    float(*red)[D] = reinterpret_cast<float(*)[D]>(&sm.stage[0][0]);
+#pragma unroll
+    for (int e = 0; e < kP; ++e) {
+      float* r = &red[warp * L::kRows + ln.row][ln.col + 2 * e];
+      r[0] = da[e].x, r[1] = da[e].y;
+      r[ln.gap] = db[e].x, r[ln.gap + 1] = db[e].y;
     }
-    r.ang.load(p, ln, pos);
-    wk.next(p);
-    if (wk.live()) pos.load(p, wk.b, wk.n);
-  };
-  auto work = [&](const Rows& r) {
-    T* dx = dx0 + r.out;
-    // dy: the transposed rotation turns the sine's sign
-    float2 ya[kUnrollBwd][kP], yb[kUnrollBwd][kP];
-    {
-      float2 ca[kP], sa[kP], cb[kP], sb[kP];
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += kTileThreads) {
+      float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < kP; ++e) {
-        ca[e] = r.ang.cosine(false, e);
-        cb[e] = r.ang.cosine(true, e);
-        const float2 s0 = r.ang.sine(false, e), s1 = r.ang.sine(true, e);
-        sa[e] = make_float2(-s0.x, -s0.y);
-        sb[e] = make_float2(-s1.x, -s1.y);
-      }
-#pragma unroll
-      for (int u = 0; u < kUnrollBwd; ++u) {
-        Half<T>::unpack(r.z[u].x, r.z[u].y, ya[u]);
-        Half<T>::unpack(r.z[u].z, r.z[u].w, yb[u]);
-        turn<L, kInter, kFull>(ln, ya[u], yb[u], ca, sa, cb, sb);
-      }
-    }
-    if (w != nullptr) {
-      float2 fa[kUnrollBwd][kP], fb[kUnrollBwd][kP];
-      float2 ga[kUnrollBwd][kP], gb[kUnrollBwd][kP];  // dy w
-      float sums[2 * kUnrollBwd];                     // of x^2 and of dy w x, per row
-#pragma unroll
-      for (int u = 0; u < kUnrollBwd; ++u) {
-        Half<T>::unpack(r.x[u].x, r.x[u].y, fa[u]);
-        Half<T>::unpack(r.x[u].z, r.x[u].w, fb[u]);
-        float2 ss = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int e = 0; e < kP; ++e) {
-          ga[u][e] = mul2(ya[u][e], wa[e]);
-          gb[u][e] = mul2(yb[u][e], wb[e]);
-          ss = fma2(fa[u][e], fa[u][e], ss);
-          ss = fma2(fb[u][e], fb[u][e], ss);
-          dot = fma2(ga[u][e], fa[u][e], dot);
-          dot = fma2(gb[u][e], fb[u][e], dot);
-        }
-        sums[u] = ss.x + ss.y;
-        sums[kUnrollBwd + u] = dot.x + dot.y;
-      }
-      static_assert(kUnrollBwd == 2, "four sums a step");
-      const float mine = sum4<L::kLanes>(sums[0], sums[1], sums[2], sums[3]);
-      const float r4 = rsqrtf(mine * (1.f / D) + p.eps);  // in the lanes that hold a sum of x^2
-#pragma unroll
-      for (int u = 0; u < kUnrollBwd; ++u) {
-        const float rn = from4<L::kLanes>(r4, u), dot = from4<L::kLanes>(mine, 2 + u);
-        const float k = -rn * rn * dot * (1.f / D);
-        const float2 rr = make_float2(rn, rn), kk = make_float2(k, k);
-        const float2 rl = live[u] ? rr : make_float2(0.f, 0.f);
-#pragma unroll
-        for (int e = 0; e < kP; ++e) {
-          da[e] = fma2(mul2(ya[u][e], rl), fa[u][e], da[e]);
-          db[e] = fma2(mul2(yb[u][e], rl), fb[u][e], db[e]);
-          ya[u][e] = mul2(rr, fma2(fa[u][e], kk, ga[u][e]));
-          yb[u][e] = mul2(rr, fma2(fb[u][e], kk, gb[u][e]));
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnrollBwd; ++u)
-      if (live[u]) ln.store(dx + oh[u], Half<T>::pack(ya[u]), Half<T>::pack(yb[u]));
-  };
-  if (wk.live()) {
-    Rows even, odd;
-    pos.load(p, wk.b, wk.n);
-    fetch(even);
-    while (true) {
-      if (!wk.live()) {
-        work(even);
-        break;
-      }
-      fetch(odd);
-      work(even);
-      if (!wk.live()) {
-        work(odd);
-        break;
-      }
-      fetch(even);
-      work(odd);
+      for (int k = 0; k < kTokens * L::kRows; ++k) sum += red[k][i];
+      p.dw[static_cast<size_t>(blockIdx.x) * D + i] = sum;
     }
   }
-  if (p.dw == nullptr) return;
-#pragma unroll
-  for (int e = 0; e < kP; ++e) {
-    float* r = &red[warp * L::kRows + ln.row][ln.col + 2 * e];
-    r[0] = da[e].x, r[1] = da[e].y;
-    r[ln.gap] = db[e].x, r[ln.gap + 1] = db[e].y;
-  }
-  if ((threadIdx.x & 31) == 0) red_side[warp] = side;
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < kWarps * L::kRows; ++k)
-      if (red_side[k / L::kRows] == i / D) sum += red[k][i % D];
-    p.dw[static_cast<size_t>(blockIdx.x) * 2 * D + i] = sum;
-  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Sum of the blocks' partial weight gradients, in a fixed order: a block of 32 x 32 threads takes
-// 32 columns.  grid (d / 32, 2).
-__global__ void __launch_bounds__(1024)
-    qk_norm_dw_kernel(const float* __restrict__ part, int blocks, int d, float* dwq, float* dwk) {
-  __shared__ float red[32][33];
+// Sum of the blocks' partial weight gradients, in a fixed order.  Block g of chunks holds queries for
+// g % chunks < cq, else keys.  A block of 8 columns x 128 rows at a time; grid (d / 8, 2).
+constexpr int kSumRows = 128;
+__global__ void __launch_bounds__(8 * kSumRows)
+    qk_norm_dw_kernel(const float* __restrict__ part, int blocks, int chunks, int cq, int d, float* dwq, float* dwk) {
+  __shared__ float red[kSumRows][9];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float* out = blockIdx.y == 0 ? dwq : dwk;
   if (out == nullptr) return;
-  const int i = threadIdx.x & 31, k = threadIdx.x >> 5, col = blockIdx.x * 32 + i;
+  const int i = threadIdx.x & 7, k = threadIdx.x >> 3, col = blockIdx.x * 8 + i;
   float t = 0.f;
-  for (int r = k; r < blocks; r += 32) t += part[(static_cast<size_t>(r) * 2 + blockIdx.y) * d + col];
+  for (int r = k; r < blocks; r += kSumRows)
+    if ((r % chunks < cq) == (blockIdx.y == 0)) t += __ldcg(part + static_cast<size_t>(r) * d + col);
   red[k][i] = t;
   __syncthreads();
-  if (k == 0) {
-    float sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < 32; ++r) sum += red[r][i];
-    out[col] = sum;
+  for (int s = kSumRows / 2; s > 0; s >>= 1) {
+    if (k < s) red[k][i] += red[k + s][i];
+    __syncthreads();
   }
+  if (k == 0) out[col] = red[0][i];
 }
 
 }  // namespace qkn

@@ -105,9 +105,10 @@ def norm_rope_bwd(x, dz, w, rope, positions, sections=None, interleaved=False, e
 
 
 def dw_bound(mag_sum, rows):
-    """A weight gradient's terms have 14 roundings; a thread adds at most rows / (296 blocks x 8
-    warps) + 8 of them in turn, its block 32 more, the last sum 10 + 32."""
-    return (14 + rows / 2368 + 8 + 32 + 42) * U * mag_sum
+    """A weight gradient's terms have 14 roundings; a thread adds at most rows / (888 blocks x 4
+    warps) + 8 of them in turn (as many blocks as there are heads allow: two thirds at least), its block 16
+    more, the last sum 7 + 7."""
+    return (14 + rows / 2368 + 8 + 16 + 14) * U * mag_sum
 
 
 def assert_within(got, ref, bound, dtype, what):
