@@ -570,6 +570,19 @@ def _one_device(stream, **tensors):
     return first.device if stream is None else _device(stream, **tensors)
 
 
+def _new(dev, stream, dtype, *shape):
+    """Memory for an output or a workspace of a call on `stream` (None: the current one), taken from
+    that stream's pool: what the current stream freed last may still be in use there."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
 def _call(fn, where, dev, stream, *args):
     """fn(*args, stream) with dev current; raises on a status."""
     import torch
@@ -638,13 +651,13 @@ def attn_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, gr
                       seq_lens=seq_lens, o=o, lse=lse, workspace=workspace)
     max_prefix_len, max_seq_len = int(max_prefix_len), int(max_seq_len)
     if o is None:
-        o = torch.empty_like(q)
+        o = _new(dev, stream, torch.bfloat16, B, Hq, 1, d)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = _new(dev, stream, torch.float32, B, Hq)
     if workspace is None:
         nbytes = attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len,
                                                            max_seq_len, d)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        workspace = _new(dev, stream, torch.uint8, max(nbytes, 16))
     _call(lib().attn_decode_shared_prefix, "attn_decode_shared_prefix", dev, stream, q.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), _at(lse), prefix_table.data_ptr(),
           prefix_lens.data_ptr(), group_starts.data_ptr(), block_table.data_ptr(),
@@ -746,8 +759,6 @@ def attn_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, sections=None, 
 
     Returns (q_out, k_out), contiguous unless given; an output may be its input.
     """
-    import torch
-
     s = _QkShapes(q, k, q_weight, k_weight, rope, positions, sections)
     if q_out is not None:
         _expect_view(q_out, "q_out", s.dtype, s.q_shape, written=True)
@@ -756,9 +767,9 @@ def attn_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, sections=None, 
     dev = _one_device(stream, q=q, k=k, q_weight=q_weight, k_weight=k_weight, rope=rope,
                       positions=positions, q_out=q_out, k_out=k_out)
     if q_out is None:
-        q_out = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
+        q_out = _new(dev, stream, s.dtype, *s.q_shape)
     if k_out is None:
-        k_out = torch.empty(s.k_shape, dtype=s.dtype, device=dev)
+        k_out = _new(dev, stream, s.dtype, *s.k_shape)
     _call(lib().attn_qk_norm_rope, "attn_qk_norm_rope", dev, stream, q.data_ptr(), k.data_ptr(),
           q_out.data_ptr(), k_out.data_ptr(), _at(q_weight), _at(k_weight), rope.data_ptr(),
           positions.data_ptr(), _longs(_bhn(q), _bhn(k), _bhn(q_out), _bhn(k_out), s.pos), s.sections,
@@ -799,16 +810,15 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope, positi
                       k_weight=k_weight, rope=rope, positions=positions, dq=dq, dk=dk,
                       dq_weight=dq_weight, dk_weight=dk_weight, workspace=workspace)
     if dq is None:
-        dq = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
+        dq = _new(dev, stream, s.dtype, *s.q_shape)
     if dk is None:
-        dk = torch.empty(s.k_shape, dtype=s.dtype, device=dev)
+        dk = _new(dev, stream, s.dtype, *s.k_shape)
     if dq_weight is None and q_weight is not None:
-        dq_weight = torch.empty(s.d, dtype=torch.float32, device=dev)
+        dq_weight = _new(dev, stream, torch.float32, s.d)
     if dk_weight is None and k_weight is not None:
-        dk_weight = torch.empty(s.d, dtype=torch.float32, device=dev)
+        dk_weight = _new(dev, stream, torch.float32, s.d)
     if workspace is None:
-        workspace = torch.empty(max(attn_qk_norm_rope_bwd_workspace_bytes(s.d), 16),
-                                dtype=torch.uint8, device=dev)
+        workspace = _new(dev, stream, torch.uint8, max(attn_qk_norm_rope_bwd_workspace_bytes(s.d), 16))
     _call(lib().attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd", dev, stream, q.data_ptr(), k.data_ptr(),
           dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _at(q_weight),
           _at(k_weight), _at(dq_weight), _at(dk_weight), rope.data_ptr(), positions.data_ptr(),
@@ -842,7 +852,7 @@ def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, rope, positions, slots,
     dev = _one_device(stream, q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, rope=rope,
                       positions=positions, slots=slots, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
     if q_out is None:
-        q_out = torch.empty(s.q_shape, dtype=s.dtype, device=dev)
+        q_out = _new(dev, stream, s.dtype, *s.q_shape)
     _call(lib().attn_qk_norm_rope_paged, "attn_qk_norm_rope_paged", dev, stream, q.data_ptr(), k.data_ptr(),
           v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _at(q_weight),
           _at(k_weight), rope.data_ptr(), positions.data_ptr(), slots.data_ptr(),
@@ -887,13 +897,13 @@ def attn_page_update(block_table, old_lens, new_lens, free_pages, ring, page_siz
                       free_pages=free_pages, ring=ring, pos_offset=pos_offset, ring_out=ring_out,
                       cu_seqlens=cu_seqlens, slots=slots, positions=positions)
     if ring_out is None:
-        ring_out = torch.empty(3, dtype=torch.int64, device=dev)
+        ring_out = _new(dev, stream, torch.int64, 3)
     if cu_seqlens is None:
-        cu_seqlens = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        cu_seqlens = _new(dev, stream, torch.int32, B + 1)
     if slots is None:
-        slots = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+        slots = _new(dev, stream, torch.int32, max_tokens)
     if positions is None:
-        positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+        positions = _new(dev, stream, torch.int32, max_tokens)
     _call(lib().attn_page_update, "attn_page_update", dev, stream, block_table.data_ptr(),
           old_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), ring.data_ptr(),
           ring_out.data_ptr(), cu_seqlens.data_ptr(), slots.data_ptr(), positions.data_ptr(),

@@ -1092,7 +1092,7 @@ bool view_ok(const void* base, const long long* st, int B, int H, int N, int siz
          (N <= 1 || (st[2] & mask) == 0);
 }
 
-qkn::View make_view(const long long* st) { return qkn::View{st[0], st[1], st[2]}; }
+qkn::View make_view(const long long* st) { return qkn::View{st[1], st[2]}; }  // (b, h, n) of a packed view
 
 // Argument rules shared by the norm + rotation calls; fills what they share of the parameters.
 int qkn_common(qkn::Params& p, const void* q_weight, const void* k_weight, const float* rope,

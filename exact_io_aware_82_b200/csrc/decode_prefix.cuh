@@ -98,8 +98,8 @@ struct Params {
   float c;                  // scale * log2(e), never 0
   float* ws_o;              // partial outputs [rows][128], then
   float* ws_lse;            // their log-sum-exps [rows]
-  int* plan;                // [0] share of a wide CTA, [1] of a thin CTA, [2] wide CTAs, [3] -, then
-                            // positions on the lines: of each group's wide jobs [num_groups], of its
+  int* plan;                // [0] share of a wide CTA, [1] of a thin CTA, [2] wide CTAs, [3] whether the
+                            // prefixes count (the groups are in order), then positions on the lines: of each group's wide jobs [num_groups], of its
                             // thin jobs [num_groups], of each sequence's own jobs [B]
   long long thin_row0, own_row0;  // first rows of the thin prefix parts and of the own parts
 };
@@ -1051,7 +1051,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mine.z += p.Hkv * thin_job(p, tiles);
     mine.w += p.Hkv * tiles;
   }
+  bool in_order = true;
   for (int g = g0; g < g1; ++g) {
+    in_order = in_order && __ldg(p.group_starts + g) <= __ldg(p.group_starts + g + 1);
     const Group gr = g == g0 ? first : load_group(p, g);
     mine.x += group_wide(p, gr);
     mine.y += group_thin(p, gr);
@@ -1109,7 +1111,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (lane == 31) sm.scan[warp] = run;
   dev::tc_fence_before();
-  __syncthreads();
+  // Groups out of order could overlap, and their sums and rows leave their bounds: no prefix counts then.
+  const bool ordered = __syncthreads_and(in_order) != 0;
   dev::tc_fence_after();
   int4 all = make_int4(0, 0, 0, 0), at = make_int4(run.x - mine.x, run.y - mine.y, run.z - mine.z, 0);
 #pragma unroll
@@ -1118,6 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (w < warp) at.x += s.x, at.y += s.y, at.z += s.z;
     all.x += s.x, all.y += s.y, all.z += s.z, all.w += s.w;
   }
+  if (!ordered) all.x = all.y = 0;
   at.z += all.y;  // own jobs stand behind the thin prefix jobs
   const int ctas = gridDim.x, cost_wide = all.x, cost_thin = all.y + all.z;
   // The time everything takes, if well divided: what the SMs need, but not less than HBM.  The wide
@@ -1151,6 +1155,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     p.plan[0] = share_wide;
     p.plan[1] = share_thin;
     p.plan[2] = wide;
+    p.plan[3] = ordered ? 1 : 0;
+    if (!ordered) atomicExch(&g_device_error, ATTN_ERR_INVALID_ARG);
   }
   auto begins = [&](int kind, int i, int pos, int cost) {
     if (cost > 0 && ct.lo >= pos && ct.lo < pos + cost) {
@@ -1160,7 +1166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
   auto inside = [&](int from, int cost) { return cost > 0 && ct.lo >= from && ct.lo < from + cost; };
-  if (writer || (is_wide ? inside(at.x, mine.x) : inside(at.y, mine.y))) {
+  if (ordered && (writer || (is_wide ? inside(at.x, mine.x) : inside(at.y, mine.y)))) {
     int x = at.x, y = at.y;
     for (int g = g0; g < g1; ++g) {
       const Group gr = g == g0 ? first : load_group(p, g);
@@ -1254,6 +1260,7 @@ __global__ void __launch_bounds__(G >= 4 ? 32 * G : 128)
   // ---- what the other kernel left ----
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int share_wide = __ldcg(p.plan), share_thin = __ldcg(p.plan + 1);
+  if (__ldcg(p.plan + 3) == 0) gr.tiles = 0;
   const int pos_prefix = gr.tiles > 0 ? __ldcg(p.plan + 4 + (thin ? p.num_groups : 0) + g) : 0;
   const int pos_own = __ldcg(p.plan + 4 + 2 * p.num_groups + b);
   Parts x0, x1;  // of the prefix job, of the own job

@@ -42,9 +42,9 @@ constexpr int kUnrollBwd = 2;  // backward: of x and of dz
 constexpr int kBlocks = 3;     // per SM, paged form: 80 registers a thread
 constexpr int kMaxAxes = 4;
 
-// Element strides of a [B][H][N][d] view (d contiguous).
+// Element strides of a packed [N][H][d] view (d contiguous).
 struct View {
-  long long b, h, n;
+  long long h, n;
 };
 
 struct Params {

@@ -355,8 +355,8 @@ ATTN_API int attn_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_
  *   q, q_out  [T][Hq][d];  k, v  [T][Hkv][d] views;  positions int32 [num_axes][T].
  *   k_cache, v_cache  bf16 [num_pages][page_size][Hkv][d], contiguous; page_size as attn_decode_paged.
  *   slots     int32 [T]: token t is written to row slots[t] of the cache's num_pages * page_size rows.
- *             A token with a negative slot is left out (nothing of it is read or written, q_out
- *             included): the padding of a fixed token count.  A slot past the cache is not followed
+ *             A token with a negative slot is left out (nothing of it is written, q_out included): the
+ *             padding of a fixed token count.  A slot past the cache is not followed
  *             either, and the device flag records ATTN_ERR_INVALID_ARG.  Slots of one call are
  *             distinct; of two tokens with one slot, which one the row ends with is not specified.
  *   strides   HOST long long [13]: (unused, h, t) of q, k, v, q_out, then the axis stride of positions.
@@ -414,7 +414,8 @@ ATTN_API int attn_page_update(int *block_table, const int *old_lens, const int *
  *   lse          fp32 [B][Hq] or NULL, over prefix and own keys.
  *   group_starts int32 [num_groups + 1] (device), non-decreasing: sequences [group_starts[g],
  *                group_starts[g + 1]) share prefix g; sequences before the first and from the last
- *                entry on have none.  Clamped to [0, B].
+ *                entry on have none.  Clamped to [0, B]; where an entry is smaller than the one before it
+ *                no prefix counts, and the device flag records ATTN_ERR_INVALID_ARG.
  *   prefix_table int32 [num_groups][max_prefix_pages], prefix_lens int32 [num_groups]: the pages and
  *                the keys of each prefix, in the same cache; lengths are clamped on the device to
  *                [0, max_prefix_len], and max_prefix_len must not exceed max_prefix_pages * page_size.
@@ -422,8 +423,9 @@ ATTN_API int attn_page_update(int *block_table, const int *old_lens, const int *
  *   prefix's) last key is not used, infinities and NaN included.
  *   workspace    device scratch of at least attn_decode_shared_prefix_workspace_bytes(...) bytes,
  *                16-byte aligned, overwritten before it is read.
- * G = Hq / Hkv in {1, 2, 4, 8}, d == 128.  Errors, and page numbers outside the cache, as
- * attn_decode_paged.  The result does not depend on scheduling (no atomics, no counter: captured
+ * G = Hq / Hkv in {1, 2, 4, 8}, d == 128, B <= 65535, and steps and partial rows that 32 bits count
+ * (ATTN_ERR_UNSUPPORTED otherwise; the workspace size is 0 for arguments that the call refuses).
+ * Errors, and page numbers outside the cache, as attn_decode_paged.  The result does not depend on scheduling (no atomics, no counter: captured
  * graphs with workspaces of their own may run at the same time).
  */
 ATTN_API size_t attn_decode_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int num_groups,

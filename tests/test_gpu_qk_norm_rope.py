@@ -264,6 +264,65 @@ def test_backward_is_the_same_every_time_and_on_another_stream():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("B,N", [(70, 1), (1, 3), (3, 2), (5, 4), (2, 5)])
+def test_short_sequences_and_single_tokens(B, N):
+    # one token a sequence, and fewer tokens than a tile holds; positions per sequence and shared
+    g = gen(15)
+    q, k = fused(g, B, N, 8, 4, 128, BF)
+    wq, wk = weight(g, 128, BF), weight(g, 128, BF)
+    rope = R.rope_table(64, 128).cuda()
+    dz = normal(g, B, 8, N, 128), normal(g, B, 4, N, 128)
+    for batch in (True, False):
+        pos = positions_for(g, B, N, None, 64, batch)
+        z = A.attn_qk_norm_rope(q, k, wq, wk, rope, pos)
+        out = A.attn_qk_norm_rope_bwd(q, k, *dz, wq, wk, rope, pos)
+        for i, (x, w) in enumerate(((q, wq), (k, wk))):
+            ref, bound = R.norm_rope(x, w, rope, pos)
+            R.assert_within(z[i], ref, bound, BF, "forward")
+            ref, bound, rdw, mag = R.norm_rope_bwd(x, dz[i], w, rope, pos)
+            R.assert_within(out[i], ref, bound, BF, "backward")
+            R.assert_within(out[2 + i], rdw, R.dw_bound(mag, B * N * x.shape[1]), F32, "weight")
+
+
+def test_outputs_leave_their_surroundings_alone():
+    # strided outputs inside larger buffers, heads and tokens that do not fill the last tile
+    g = gen(16)
+    B, N, Hq, Hkv = 2, 11, 9, 3
+    q, k = fused(g, B, N, Hq, Hkv, 128, BF)
+    w = weight(g, 128, BF)
+    rope = R.rope_table(16, 128).cuda()
+    pos = torch.arange(N, dtype=torch.int32).cuda()
+    buf = torch.full((B, N + 2, Hq + Hkv + 2, 192), 9.0, dtype=BF, device="cuda")
+    qo = buf[:, 1:-1, 1:1 + Hq, 32:160].transpose(1, 2)
+    ko = buf[:, 1:-1, 1 + Hq:-1, 32:160].transpose(1, 2)
+    want = A.attn_qk_norm_rope(q, k, w, w, rope, pos)
+    A.attn_qk_norm_rope(q, k, w, w, rope, pos, q_out=qo, k_out=ko)
+    torch.cuda.synchronize()
+    assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+    qo.fill_(9.0), ko.fill_(9.0)
+    assert torch.all(buf == 9.0)
+
+
+def test_offsets_past_32_bits():
+    # a projection output of 6 GB: rows behind the first 4 GB
+    N, H = 12000, 1000
+    x = torch.zeros(1, N, 2 * H, 128, dtype=BF, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(17)
+    x[0, -5:] = torch.randn(5, 2 * H, 128, generator=g, device="cuda").to(BF)
+    q, k = x[:, :, :H].transpose(1, 2), x[:, :, H:].transpose(1, 2)
+    w = torch.ones(128, dtype=BF, device="cuda")
+    rope = R.rope_table(N, 128).cuda()
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    ref_q, bq = R.norm_rope(q[:, :, -5:], w, rope, pos[-5:])
+    ref_k, bk = R.norm_rope(k[:, :, -5:], w, rope, pos[-5:])
+    A.attn_qk_norm_rope(q, k, w, w, rope, pos, q_out=q, k_out=k)
+    torch.cuda.synchronize()
+    R.assert_within(q[:, :, -5:], ref_q, bq, BF, "q")
+    R.assert_within(k[:, :, -5:], ref_k, bk, BF, "k")
+    assert torch.all(x[0, :-5] == 0)
+
+
 def paged_case(seed, T, pad, Hq, Hkv, page, rot=128, sections=None, inter=False):
     g = gen(seed)
     qkv = normal(g, T, Hq + 2 * Hkv, 128, scale=1.5)

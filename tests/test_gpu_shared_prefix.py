@@ -206,6 +206,50 @@ def test_agrees_with_paged_decode():
     assert (lse - pl).abs().max() <= 1e-4
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    # cuts of the lines at random places: wide, half-wide and thin blocks of groups beside own keys
+    rng = np.random.default_rng(200 + seed)
+    g = int(rng.choice([1, 2, 4, 8]))
+    hkv = int(rng.choice([1, 2, 3, 5]))
+    B = int(rng.integers(1, 200))
+    n = int(rng.integers(0, min(B, 6) + 1))
+    starts = sorted(rng.integers(0, B + 1, n + 1).tolist())
+    plens = [int(x) for x in rng.choice([0, 1, 127, 128, 129, 700, 1500, 4000], n)]
+    lens = [int(x) for x in np.where(rng.random(B) < 0.3, rng.integers(0, 1500, B), rng.integers(0, 150, B))]
+    page = int(rng.choice([8, 16, 32, 64, 128, 256]))
+    c = case(300 + seed, B, hkv * g, hkv, starts, plens, lens, page)
+    o, lse = A.attn_decode_shared_prefix(**c)
+    torch.cuda.synchronize()
+    assert A.attn_get_device_error() == 0
+    check(c, starts, plens, lens, o, lse, some=sorted(set(rng.integers(0, B, 24).tolist() + [0, B - 1])))
+
+
+def test_groups_out_of_order_are_flagged_and_no_prefix_counts():
+    lens = [5, 60, 7, 300]
+    c = case(133, 4, 8, 2, [0, 2, 4], [70, 900], lens, 16)
+    c["group_starts"].copy_(torch.tensor([0, 4, 1]))
+    o, lse = A.attn_decode_shared_prefix(**c)
+    assert A.attn_get_device_error() == A.ATTN_ERR_INVALID_ARG
+    check(c, [0, 0, 0], [70, 900], lens, o, lse)
+
+
+def test_on_another_stream_without_a_workspace():
+    starts, plens, lens = [0, 30], [1000], own_lens(7, 30)
+    c = case(134, 30, 16, 4, starts, plens, lens, 32)
+    ref, ref_l = A.attn_decode_shared_prefix(**c)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs = [A.attn_decode_shared_prefix(**c, stream=s, return_lse=False) for _ in range(4)]
+    s.synchronize()
+    for o, lse in outs:
+        assert lse is None and torch.equal(o, ref)
+    o, lse = torch.empty_like(ref), torch.empty_like(ref_l)
+    got = A.attn_decode_shared_prefix(**c, o=o, lse=lse)
+    torch.cuda.synchronize()
+    assert got[0] is o and got[1] is lse and torch.equal(o, ref) and torch.equal(lse, ref_l)
+
+
 def test_large_batch_and_long_prefix():
     B, plen = 256, 16384
     lens = own_lens(4, B)
