@@ -1243,8 +1243,8 @@ int pfx_shapes(int B, int Hq, int Hkv, int num_groups, int max_prefix_len, int m
   const double blocks = std::min<double>(B, B / (256 / G) + static_cast<double>(num_groups));
   const double cost = Hkv * (blocks * ((max_prefix_len / 128 + 1.0) * pfx::kCostBoth + pfx::kCostWideJob) +
                              static_cast<double>(B) * ((max_seq_len / 128 + 1.0) * pfx::kCostThinMax + pfx::kCostThinJob));
-  // grid (Hkv, B) of the joining kernel, and partial rows in 32 bits
-  if (B > 65535 || 6.0 * B * Hq + 148.0 * 512 > 2.0e9) return ATTN_ERR_UNSUPPORTED;
+  // grid (Hkv, B) of the joining kernel, and its 16-byte units of partial rows in 32 bits
+  if (B > 65535 || (6.0 * B * Hq + 148.0 * 512) * 32 > 2.0e9) return ATTN_ERR_UNSUPPORTED;
   return cost < 2.0e9 ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
 }
 
@@ -1597,10 +1597,22 @@ int attn_decode_shared_prefix(const void* q, const void* k_cache, const void* v_
   else
     pfx::decode_prefix_kernel<false><<<ctas, pfx::kThreads, pfx::kSmemBytes, st>>>(tq, tq_thin, tq_own, tk, tv, p);
   if ((rc = cuda_status(cudaGetLastError())) != ATTN_OK) return rc;
-  void (*combine)(pfx::Params, __nv_bfloat16*, float*) =
-      p.G == 1 ? pfx::decode_prefix_combine_kernel<1> : p.G == 2 ? pfx::decode_prefix_combine_kernel<2>
-      : p.G == 4 ? pfx::decode_prefix_combine_kernel<4> : pfx::decode_prefix_combine_kernel<8>;
-  return launch_early<pfx::Params, __nv_bfloat16*, float*>(combine, dim3(Hkv, B), std::max(32 * p.G, 128), st, p,
+  // sets of warps per block: as many as the SMs hold at 32 warps each
+  int split = 4;
+  while (split > 1 && static_cast<long long>(B) * Hq * split > 32ll * info->num_sms) split /= 2;
+  void (*combine)(pfx::Params, __nv_bfloat16*, float*) = nullptr;
+#define ATTN_PFX_COMBINE(G)                                                  \
+  combine = split == 4   ? pfx::decode_prefix_combine_kernel<G, 4>           \
+            : split == 2 ? pfx::decode_prefix_combine_kernel<G, 2>           \
+                         : pfx::decode_prefix_combine_kernel<G, 1>
+  switch (p.G) {
+    case 1: ATTN_PFX_COMBINE(1); break;
+    case 2: ATTN_PFX_COMBINE(2); break;
+    case 4: ATTN_PFX_COMBINE(4); break;
+    default: ATTN_PFX_COMBINE(8); break;
+  }
+#undef ATTN_PFX_COMBINE
+  return launch_early<pfx::Params, __nv_bfloat16*, float*>(combine, dim3(Hkv, B), 32 * p.G * split, st, p,
                                                            static_cast<__nv_bfloat16*>(o), lse);
 }
 

@@ -1126,19 +1126,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ctas = gridDim.x, cost_wide = all.x, cost_thin = all.y + all.z;
   // The time everything takes, if well divided: what the SMs need, but not less than HBM.  The wide
   // line gets the CTAs that finish it in that time, the thin line the others.
-  // (unsigned 32 bits: the host admits no sum of costs past 2^31)
-  const unsigned hbm = static_cast<unsigned>(all.w) / kHbmDen * kHbmNum;
-  const unsigned need = (static_cast<unsigned>(cost_wide) + cost_thin + ctas - 1) / ctas;
-  const unsigned time = max(max(hbm, need), 1u);
-  int wide = min(static_cast<int>((cost_wide + time - 1) / time), ctas);
+  // Quotients are approximations (an integer division is a hundred clocks of a few on the way to the first
+  // load): every CTA computes the same ones, and a share is rounded up past their error.
+  const float time = fmaxf(fmaxf(static_cast<float>(all.w) * (static_cast<float>(kHbmNum) / kHbmDen),
+                                 __fdividef(static_cast<float>(cost_wide) + static_cast<float>(cost_thin), ctas)),
+                           1.f);
+  auto split = [](int cost, float by) { return static_cast<int>(__fdividef(static_cast<float>(cost), by) * 1.000001f) + 1; };
+  int wide = cost_wide > 0 ? min(split(cost_wide, time), ctas) : 0;
   if (cost_thin > 0) wide = min(wide, ctas - 1);
   if (cost_thin == 0) wide = ctas;
   // every CTA between a job's first and last holds at least one of its steps: a share is not
   // shorter than a step
-  const int share_wide =
-      max(wide > 0 ? static_cast<int>((static_cast<unsigned>(cost_wide) + wide - 1) / wide) : 0, kCostBoth);
-  const int share_thin = max(
-      wide < ctas ? static_cast<int>((static_cast<unsigned>(cost_thin) + ctas - wide - 1) / (ctas - wide)) : 0, p.thin_cost);
+  const int share_wide = max(wide > 0 ? split(cost_wide, wide) : 0, kCostBoth);
+  const int share_thin = max(wide < ctas ? split(cost_thin, ctas - wide) : 0, p.thin_cost);
   const bool is_wide = static_cast<int>(blockIdx.x) < wide;
   Cta ct;
   ct.sm = &sm;
@@ -1215,28 +1215,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Join the parts: one block per (kv head, sequence), kSplit warps for each of its G query rows, four
-// columns a lane.  A row's parts from one job are numbered in line order: part e is in the job's e / h-th
-// CTA, h = 2 where the job's parts come in halves (even and odd steps or chunks; a half that holds
-// nothing has a log-sum-exp of -infinity), else 1.
+// Join the parts: one block per (kv head, sequence).  A warp takes the G query rows together, so that it
+// reads whole sectors of either layout of the parts: lane = row + G * (16-byte column), G warps for all
+// columns; kSplit such sets of warps (as many as the SMs hold) share the parts out, 32 / G of them in
+// a round.  A round's values are loaded beside its log-sum-exps, not behind them.
+// A row's parts from one job are numbered in line order: part e is in the job's e / h-th CTA, h = 2
+// where the job's parts come in halves (even and odd steps or chunks; a half that holds nothing has a
+// log-sum-exp of -infinity), else 1.
 struct Parts {
   int first, ctas, halves;
-  int row;        // the query row's first partial row in CTA 0 of the line
+  int row;        // the part's first row in CTA 0 of the line
   int cta_rows;   // rows from one CTA's part to the next one's
   int half_rows;  // rows from the first half to the second
-  int in, rows;   // wide: row within the part, rows of the part; thin: rows = 0
+  int in, rows;   // the first query row within the part; wide: rows of the part, thin: 0
 };
 
-template <int G>
-__global__ void __launch_bounds__(G >= 4 ? 32 * G : 128)
+template <int G, int kSplit>
+__global__ void __launch_bounds__(32 * G * kSplit)
     decode_prefix_combine_kernel(const Params p, __nv_bfloat16* __restrict__ o,
                                  float* __restrict__ lse) {
-  constexpr int kSplit = G >= 4 ? 1 : 4 / G;
-  constexpr int kLoads = 8;  // parts on their way at once
+  constexpr int kRound = 32 / G;                  // parts of a round
+  constexpr int kLoads = kRound < 8 ? kRound : 8;  // values on their way at once
   __shared__ float4 sum[kSplit > 1 ? G * kSplit : 1][32];
-  __shared__ float zsum[kSplit > 1 ? G * kSplit : 1];
+  __shared__ float2 stat[kSplit > 1 ? kSplit : 1][G];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = warp / kSplit, part0 = warp % kSplit;
+  const int r = lane % G, part0 = warp / G;
+  const int col = (warp % G) * kRound + lane / G;  // in units of 4 columns
   const int hk = blockIdx.x, b = blockIdx.y;
 
   // ---- inputs of the call: the group of the sequence is the last one that starts at or before it ----
@@ -1280,11 +1284,11 @@ __global__ void __launch_bounds__(G >= 4 ? 32 * G : 128)
   if (gr.tiles > 0) {
     const int n = blk < gr.full ? kBlockSeqs : gr.rest;
     x0.row = 2 * G * (p.Hkv * (gr.b0 + blk * kBlockSeqs) + n * hk);
-    x0.in = (in % kBlockSeqs) * G + r;
+    x0.in = (in % kBlockSeqs) * G;
     x0.half_rows = n * G;
     if (thin) {
       x0.halves = 2;
-      x0.row += static_cast<int>(p.thin_row0) + x0.in;
+      x0.row += static_cast<int>(p.thin_row0);
       x0.cta_rows = kThinCtaRows;
       x0.rows = 0;
       span(x0, pos_prefix + hk * thin_job(p, gr.tiles), gr.tiles, p.thin_cost, share_thin);
@@ -1299,14 +1303,13 @@ __global__ void __launch_bounds__(G >= 4 ? 32 * G : 128)
         x0.in -= 128;
         x0.rows = n * G - 128;
       }
-      x0.row += x0.in;
       span(x0, pos_prefix + p.Hkv * blk * wide_job(gr.tiles, kCostBoth) + hk * wide_job(gr.tiles, w), gr.tiles, w,
            share_wide);
     }
   }
   if (own_tiles > 0) {
     x1.halves = 2;
-    x1.row = static_cast<int>(p.own_row0) + 2 * G * (b * p.Hkv + hk) + r;
+    x1.row = static_cast<int>(p.own_row0) + 2 * G * (b * p.Hkv + hk);
     x1.cta_rows = 2 * G;
     x1.half_rows = G;
     x1.rows = x1.in = 0;
@@ -1314,73 +1317,78 @@ __global__ void __launch_bounds__(G >= 4 ? 32 * G : 128)
   }
   const int n0 = x0.halves * x0.ctas, n1 = 2 * x1.ctas;
   const float4* src = reinterpret_cast<const float4*>(p.ws_o);
-  float top = neg_inf(), z = 0.f;
+  float top = neg_inf(), z = 0.f;  // of row r
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  // 32 parts of the row at a time: a lane reads one part's log-sum-exp, then the row's warps add up
-  // every kSplit-th part each
-  for (int e0 = 0; e0 < n0 + n1; e0 += 32) {
-    int e = e0 + lane, row = 0, step = 0;
-    long long off = 0;
+  for (int e0 = part0 * kRound; e0 < n0 + n1; e0 += kSplit * kRound) {
+    // this lane's part of the round: where its values begin, their step from column to column and from row to
+    // row (in units of 4 floats), and row r's log-sum-exp
+    int e = e0 + lane / G, at = 0, step = 0, next = 0;
     float L = neg_inf();
     if (e < n0 + n1) {
       const bool first = e < n0;
       if (!first) e -= n0;
       const int halves = first ? x0.halves : 2, h = halves == 2 ? e & 1 : 0, cta = halves == 2 ? e >> 1 : e;
-      row = (first ? x0.row : x1.row) + ((first ? x0.first : x1.first) + cta) * (first ? x0.cta_rows : x1.cta_rows) +
-            (h ? (first ? x0.half_rows : x1.half_rows) : 0);
-      const int rows = first ? x0.rows : 0;
-      // 16-byte units: a wide part holds 16 bytes of every row after 16 bytes of every row
-      off = rows > 0 ? static_cast<long long>(row - x0.in) * (kD / 4) + x0.in : static_cast<long long>(row) * (kD / 4);
+      const int row = (first ? x0.row : x1.row) + ((first ? x0.first : x1.first) + cta) * (first ? x0.cta_rows : x1.cta_rows) +
+                      (h ? (first ? x0.half_rows : x1.half_rows) : 0);
+      const int rows = first ? x0.rows : 0, inside = first ? x0.in : 0;
+      L = __ldcg(p.ws_lse + row + inside + r);
+      // a wide part holds 16 bytes of every row after 16 bytes of every row
+      at = row * (kD / 4) + (rows > 0 ? inside : inside * (kD / 4));
       step = rows > 0 ? rows : 1;
-      L = __ldcg(p.ws_lse + row);
+      next = rows > 0 ? 1 : kD / 4;
     }
-    float mx = L;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-    const float new_top = fmaxf(top, mx);
-    const float f = new_top == neg_inf() ? 1.f : __expf(top - new_top);
-    z *= f;
-    acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
-    top = new_top;
-    // a NaN part (NaN inputs) stays NaN; a part that holds nothing is not read
-    const float wgt = L == neg_inf() ? 0.f : __expf(L - top);
-    unsigned live = __ballot_sync(0xffffffffu, !(L == neg_inf()));
-    if (kSplit > 1) live &= (kSplit == 4 ? 0x11111111u : 0x55555555u) << part0;
-    while (live) {
+    const int parts = min(kRound, n0 + n1 - e0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < parts; i0 += kLoads) {
       float4 v[kLoads];
-      float w[kLoads];
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const bool on = live != 0;
-        const int from = on ? __ffs(live) - 1 : 0;
-        live &= live - 1;
-        const long long a = __shfl_sync(0xffffffffu, off, from);
-        const int st = __shfl_sync(0xffffffffu, step, from);
-        w[i] = __shfl_sync(0xffffffffu, wgt, from);
-        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) v[i] = src[a + lane * st];
-        else w[i] = 0.f;
+        const int from = ((i0 + i) * G) & 31;
+        const int a = __shfl_sync(0xffffffffu, at, from), st = __shfl_sync(0xffffffffu, step, from);
+        const int nx = __shfl_sync(0xffffffffu, next, from);
+        v[i] = i0 + i < parts ? src[a + col * st + r * nx] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (i0 == 0) {
+        float mx = L;
+#pragma unroll
+        for (int s = 16; s >= G; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+        const float new_top = fmaxf(top, mx);
+        const float f = new_top == neg_inf() ? 1.f : __expf(top - new_top);
+        z *= f;
+        acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+        top = new_top;
+        L = L == neg_inf() ? 0.f : __expf(L - top);  // the part's weight; of NaN parts (NaN inputs) NaN
       }
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        z += w[i];
-        acc.x = fmaf(w[i], v[i].x, acc.x);
-        acc.y = fmaf(w[i], v[i].y, acc.y);
-        acc.z = fmaf(w[i], v[i].z, acc.z);
-        acc.w = fmaf(w[i], v[i].w, acc.w);
+        const float w = __shfl_sync(0xffffffffu, L, (((i0 + i) * G) & 31) + r);
+        if (i0 + i < parts && !(w == 0.f)) {  // a part that holds nothing was never written
+          z += w;
+          acc.x = fmaf(w, v[i].x, acc.x);
+          acc.y = fmaf(w, v[i].y, acc.y);
+          acc.z = fmaf(w, v[i].z, acc.z);
+          acc.w = fmaf(w, v[i].w, acc.w);
+        }
       }
     }
   }
-  if constexpr (kSplit > 1) {  // (every warp of the row has the same maximum)
+  if constexpr (kSplit > 1) {
     sum[warp][lane] = acc;
-    if (lane == 0) zsum[warp] = z;
+    if (warp % G == 0 && lane < G) stat[part0][r] = make_float2(top, z);
     __syncthreads();
     if (part0 != 0) return;
+    top = neg_inf();
 #pragma unroll
-    for (int k = 1; k < kSplit; ++k) {
-      const float4 v = sum[warp + k][lane];
-      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-      z += zsum[warp + k];
+    for (int k = 0; k < kSplit; ++k) top = fmaxf(top, stat[k][r].x);
+    z = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kSplit; ++k) {
+      const float2 t = stat[k][r];
+      const float f = t.x == top ? 1.f : __expf(t.x - top);  // (also where no warp has a part)
+      const float4 v = sum[warp + k * G][lane];
+      z = fmaf(f, t.y, z);
+      acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y), acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
     }
   }
   const long long bh = (static_cast<long long>(b) * p.Hkv + hk) * G + r;
@@ -1388,8 +1396,8 @@ __global__ void __launch_bounds__(G >= 4 ? 32 * G : 128)
   uint2 out;
   out.x = dev::pack_bf16x2(acc.x * inv, acc.y * inv);
   out.y = dev::pack_bf16x2(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(o + bh * kD + 4 * lane) = out;
-  if (lane == 0 && lse != nullptr) lse[bh] = z == 0.f ? neg_inf() : top + logf(z);
+  *reinterpret_cast<uint2*>(o + bh * kD + 4 * col) = out;
+  if (col == 0 && lse != nullptr) lse[bh] = z == 0.f ? neg_inf() : top + logf(z);
 }
 
 }  // namespace pfx
