@@ -311,25 +311,31 @@ __device__ __forceinline__ void wide_produce(const CUtensorMap& tm_q, const CUte
     }
     __syncwarp();
     ++q_loads;
-    int page = pc.page(p, table, p.max_prefix_pages, key0, len);
-    for (int j = 0; j < u.nk; ++j, key0 += kTile) {
+    // Keys of step j, then its values; in alt mode the keys run a step ahead, because S does.
+    auto load = [&](bool keys, int page, int j) {
+      int& count = keys ? k_issued : v_issued;
+      const int s = count & 1, ph = (count >> 1) ^ 1, at = key0 + j * kTile;
+      const int row = pc.row(p, page, at);
+      if (!(ok = warp_wait(keys ? &sm.bar_kempty[s] : &sm.bar_vempty[s], ph, abort))) return false;
+      const uint32_t bar = dev::smem_u32(keys ? &sm.bar_kfull[s] : &sm.bar_vfull[s]);
+      if (lane == 0) dev::mbar_arrive_expect_tx(bar, pc.bytes(at, len));
+      __syncwarp();
+      pc.load(keys ? &tm_k : &tm_v, dev::smem_u32(keys ? sm.w.k[s] : sm.w.v[s]), bar, page, row, u.hk);
+      ++count;
+      return true;
+    };
+    auto page_of = [&](int j) {
+      return j < u.nk ? pc.page(p, table, p.max_prefix_pages, key0 + j * kTile, len) : -2;
+    };
+    int page = page_of(0), next = page_of(1);
+    if (!load(true, page, 0)) return;
+    for (int j = 0; j < u.nk; ++j) {
       const int cur = page;
-      page = j + 1 < u.nk ? pc.page(p, table, p.max_prefix_pages, key0 + kTile, len) : -2;
-      const int s = k_issued & 1, ph = (k_issued >> 1) ^ 1;
-      const int row = pc.row(p, cur, key0);
-      const uint32_t bytes = pc.bytes(key0, len);
-      if (!(ok = warp_wait(&sm.bar_kempty[s], ph, abort))) return;
-      const uint32_t bk = dev::smem_u32(&sm.bar_kfull[s]);
-      if (lane == 0) dev::mbar_arrive_expect_tx(bk, bytes);
-      __syncwarp();
-      pc.load(&tm_k, dev::smem_u32(sm.w.k[s]), bk, cur, row, u.hk);
-      ++k_issued;
-      if (!(ok = warp_wait(&sm.bar_vempty[s], ph, abort))) return;
-      const uint32_t bv = dev::smem_u32(&sm.bar_vfull[s]);
-      if (lane == 0) dev::mbar_arrive_expect_tx(bv, bytes);
-      __syncwarp();
-      pc.load(&tm_v, dev::smem_u32(sm.w.v[s]), bv, cur, row, u.hk);
-      ++v_issued;
+      page = next;
+      next = page_of(j + 2);
+      if (u.both && !load(false, cur, j)) return;
+      if (j + 1 < u.nk && !load(true, page, j + 1)) return;
+      if (!u.both && !load(false, cur, j)) return;
     }
   };
 

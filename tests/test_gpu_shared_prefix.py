@@ -82,6 +82,7 @@ def keys_of(c, b, starts, plens, lens):
 
 
 def check(c, starts, plens, lens, o, lse, scale=1 / math.sqrt(128), some=None):
+    assert A.attn_get_device_error() == 0  # (a wait that gave up names its test)
     for b in (some if some is not None else range(len(lens))):
         k, v = keys_of(c, b, starts, plens, lens)
         R.assert_decode(o[b, :, 0], lse[b], R.decode_reference(R.f64(c["q"][b, :, 0]), k, v, scale), "sequence %d" % b)
