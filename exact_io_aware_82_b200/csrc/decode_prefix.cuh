@@ -78,6 +78,9 @@ constexpr int kHbmNum = 5, kHbmDen = 64;
 constexpr int kThinRows = 16;   // query rows of a thin job
 constexpr int kChunk = 4;       // tiles of a thin chunk
 constexpr int kThinStages = 5;  // tiles on their way in a thin CTA
+// The values of a CTA's last chunk are all streamed before the end is published, and the tensor core
+// takes them after it has seen the end: the ring has to hold them.  (4 and 5 stages measure alike.)
+static_assert(kThinStages >= kChunk, "the last chunk's values wait in the ring");
 
 // Rows of partial results, by region: a job's rows start at 2 G Hkv (its first sequence) + 2 G n (its kv
 // head) for a block of n sequences, and every CTA adds its index times a stride that is not below

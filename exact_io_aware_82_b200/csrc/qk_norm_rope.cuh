@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_paged_kernel(c
 constexpr int kTokens = 4;
 constexpr int kTileThreads = 32 * kTokens;
 constexpr int kTileBlocks = 7;     // per SM: 72 registers a thread
-constexpr int kTileBlocksBwd = 6;  // backward: 80
+constexpr int kTileBlocksBwd = 5;  // backward: 96 (6 at 80 spill: 2% slower with several axes, else the same)
 constexpr int kStages = 3;
 constexpr int kWarpBytes = 2048;  // of a stage: a warp's rows (backward: half of them x, half dz)
 constexpr int kStageBytes = kTokens * kWarpBytes;
@@ -527,16 +527,17 @@ __device__ __forceinline__ void stream_tiles(TileSmem& sm, Tiles tl, const CUten
   };
   if (threadIdx.x == 0) {
     Tiles t = tl;
-    load(0, t);
-    t.next();
-    load(1, t);
+    for (int j = 0; j < kStages - 1; ++j, t.next()) load(j, t);
   }
   const uint32_t from = in1 != nullptr ? bytes : 0;
   bool ok = true;
   int i = 0;
   for (; tl.live(); ++i, tl.next()) {
     const int s = i % kStages;
-    ok = work(sm.stage[s], tl, [&] { return wait_bounded(dev::smem_u32(&sm.full[s]), (i / kStages) & 1, abort); });
+    // (a warp gives up as a whole: the work behind the wait exchanges values between its lanes)
+    ok = work(sm.stage[s], tl, [&] {
+      return __all_sync(0xffffffffu, wait_bounded(dev::smem_u32(&sm.full[s]), (i / kStages) & 1, abort)) != 0;
+    });
     dev::fence_proxy_async_smem();
     ok = __syncthreads_and(ok) != 0;
     if (!ok) break;
@@ -545,17 +546,15 @@ __device__ __forceinline__ void stream_tiles(TileSmem& sm, Tiles tl, const CUten
       dev::bulk_commit_group();
       dev::bulk_wait_group_read1();  // the tile before has left its stage: the one after next may come
       Tiles t = tl;
-      t.next();
-      t.next();
-      load(i + 2, t);
+      for (int j = 0; j < kStages - 1; ++j) t.next();
+      load(i + kStages - 1, t);
     }
   }
   if (threadIdx.x == 0) {
     dev::bulk_wait_group_read0();
-    if (!ok) {  // a wait gave up: the tiles i and i + 1 may still be landing
-      wait_drain(dev::smem_u32(&sm.full[i % kStages]), (i / kStages) & 1);
-      tl.next();
-      if (tl.live()) wait_drain(dev::smem_u32(&sm.full[(i + 1) % kStages]), ((i + 1) / kStages) & 1);
+    if (!ok) {  // a wait gave up: the tiles from i on may still be landing
+      for (int j = i; j < i + kStages - 1 && tl.live(); ++j, tl.next())
+        wait_drain(dev::smem_u32(&sm.full[j % kStages]), (j / kStages) & 1);
     }
   }
 }
