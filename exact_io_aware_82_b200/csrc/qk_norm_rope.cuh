@@ -749,22 +749,40 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocksBwd)
 constexpr int kSumRows = 128;
 __global__ void __launch_bounds__(8 * kSumRows)
     qk_norm_dw_kernel(const float* __restrict__ part, int blocks, int chunks, int cq, int d, float* dwq, float* dwk) {
-  __shared__ float red[kSumRows][9];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float red[32][9];
   float* out = blockIdx.y == 0 ? dwq : dwk;
   if (out == nullptr) return;
-  const int i = threadIdx.x & 7, k = threadIdx.x >> 3, col = blockIdx.x * 8 + i;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = threadIdx.x & 7, k = threadIdx.x >> 3;
+  // this side's rows in order, n of every `chunks`; this thread takes every kSumRows-th, from the k-th on
+  const int n = max(blockIdx.y == 0 ? cq : chunks - cq, 1);
+  const int step_g = kSumRows / n, step_c = kSumRows % n;
+  int g = k / n, c = k % n;
+  const int end = blocks / chunks;
+  const float* at = part + (blockIdx.y == 0 ? 0 : cq) * d + blockIdx.x * 8 + i;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float t = 0.f;
-  for (int r = k; r < blocks; r += kSumRows)
-    if ((r % chunks < cq) == (blockIdx.y == 0)) t += __ldcg(part + static_cast<size_t>(r) * d + col);
-  red[k][i] = t;
-  __syncthreads();
+  while (g < end) {
+    float v[8];
 #pragma unroll
-  for (int s = kSumRows / 2; s > 0; s >>= 1) {
-    if (k < s) red[k][i] += red[k + s][i];
-    __syncthreads();
+    for (int u = 0; u < 8; ++u) {
+      v[u] = g < end ? __ldcg(at + static_cast<size_t>(g * chunks + c) * d) : 0.f;
+      g += step_g, c += step_c;
+      if (c >= n) c -= n, ++g;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) t += v[u];
   }
-  if (k == 0) out[col] = red[0][i];
+  // the four rows of a warp, then the warps: warp w sums column w
+  t += __shfl_xor_sync(0xffffffffu, t, 8);
+  t += __shfl_xor_sync(0xffffffffu, t, 16);
+  if (lane < 8) red[warp][lane] = t;
+  __syncthreads();
+  if (warp >= 8) return;
+  t = red[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (lane == 0) out[blockIdx.x * 8 + warp] = t;
 }
 
 }  // namespace qkn
