@@ -11,10 +11,11 @@
 // 128-key tile of a job.  How a step is computed depends on the query rows of its job:
 //   both  more than 128 rows (at most 256): S = Q K^T with the rows as M, P from tensor memory for
 //         O += P V; two row tiles take every step, so a key tile read once feeds up to 256 rows.
-//         About 3900 SM clocks a step (the exponentials of 32768 weights are most of it).
+//         About 4000 SM clocks a step: scores, softmax of 32768 weights and P V follow each other in each
+//         row tile, and the two row tiles overlap only in part.
 //   alt   17 to 128 rows: the same with the two row tiles holding the same rows and taking
 //         alternate steps, so one step's softmax overlaps the next step's products; even and odd
-//         steps end as two parts.  About 2400 clocks a step.
+//         steps end as two parts.  About 2700 clocks a step.
 //   thin  at most 16 rows (every sequence's own keys among them): S^T = K Q^T with the keys as M and
 //         16 columns, O^T += V^T P^T; a thread holds a key's few scores, so a step costs far
 //         less than its 64 KB take to arrive.
@@ -412,7 +413,7 @@ __device__ __forceinline__ void wide_mma(const Cta& ct) {
   const uint64_t dv0 = dev::smem_desc(dev::smem_u32(sm.w.v[0]), kGroupHalf, kGroupBytes, dev::kSwizzle128B);
   bool ok = true;
   int taken = 0, gbase = 0;
-  int ptot[2] = {0, 0};
+  int ptot0 = 0, ptot1 = 0;
   while (ok) {
     const int slot = taken & 1;
     if (!(ok = warp_wait(&sm.bar_unit_full[slot], taken >> 1, abort))) break;
@@ -420,67 +421,54 @@ __device__ __forceinline__ void wide_mma(const Cta& ct) {
     if (!us.valid) break;
     ++taken;
     const int nk = us.nk, both = us.both, flip = us.flip, tail = us.tail;
-    int s_left = both ? 2 * nk : nk;  // S products of the run still to issue
-    // S of row tile t against the keys of step j; `last`: no other row tile reads them
-    auto issue_s = [&](int t, int j, bool last) {
-      const int g = gbase + j;
-      if (!warp_wait(&sm.bar_kfull[g & 1], g >> 1, abort)) return false;
-      dev::tc_fence_after();
-      if (lane == 0) {
-        const uint64_t a0 = dq0 + static_cast<uint64_t>(both ? t * kBufStep : 0);
-        const uint64_t b0 = dk0 + static_cast<uint64_t>((g & 1) * kBufStep);
-#pragma unroll
-        for (int ks = 0; ks < kD / 16; ++ks) {
-          const uint32_t qoff = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-          const uint32_t koff = ((ks >> 2) * kGroupHalf + (ks & 3) * 32) >> 4;
-          dev::umma_ss(tmem + t * 128, a0 + qoff, b0 + koff, idesc_s, ks > 0 ? 1u : 0u);
-        }
-        dev::umma_commit(dev::smem_u32(&sm.bar_s[t]));
-        if (s_left == 1) dev::umma_commit(dev::smem_u32(&sm.bar_qempty));
-        if (last) dev::umma_commit(dev::smem_u32(&sm.bar_kempty[g & 1]));
-      }
-      --s_left;
-      __syncwarp();
-      return true;
-    };
-    // O += P V of row tile t for step j
-    auto issue_pv = [&](int t, int j, bool acc, bool last, bool final_step) {
-      const int g = gbase + j;
-      if (!warp_wait(&sm.bar_p[t], ptot[t], abort)) return false;
-      ++ptot[t];
-      dev::tc_fence_after();
-      if (lane == 0) {
-        const uint64_t b0 = dv0 + static_cast<uint64_t>((g & 1) * kBufStep);
-#pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks)
-          dev::umma_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, b0 + ((ks * 2 * kGroupBytes) >> 4), idesc_o,
-                       (acc || ks > 0) ? 1u : 0u);
-        if (last) dev::umma_commit(dev::smem_u32(&sm.bar_vempty[g & 1]));
-        if (final_step) dev::umma_commit(dev::smem_u32(&sm.bar_o[t]));
-      }
-      __syncwarp();
-      return true;
-    };
-    // the values of step j have landed; behind the job's last key they become zeros
-    auto wait_v = [&](int j) {
-      const int g = gbase + j;
-      if (!warp_wait(&sm.bar_vfull[g & 1], g >> 1, abort)) return false;
-      if (j == nk - 1 && tail < kTile) zero_tail(dev::smem_u32(sm.w.v[g & 1]), tail);
-      return true;
-    };
+    // Item x of the run: row tile and step.  S runs two items ahead of P V.
+    const int items = both ? 2 * nk : nk;
+    auto tile_of = [&](int x) { return (x & 1) ^ flip; };
+    auto step_of = [&](int x) { return both ? x >> 1 : x; };
     ok = warp_wait(&sm.bar_q, taken - 1, abort);
-    if (both) {
-      ok = ok && issue_s(0, 0, false) && issue_s(1, 0, true);
-      for (int j = 0; ok && j < nk; ++j) {
-        const bool more = j + 1 < nk;
-        ok = wait_v(j) && issue_pv(0, j, j > 0, false, !more) && (!more || issue_s(0, j + 1, false)) &&
-             issue_pv(1, j, j > 0, true, !more) && (!more || issue_s(1, j + 1, true));
+#pragma unroll 1
+    for (int x = 0; ok && x < items + 2; ++x) {
+      if (x >= 2) {
+        // O += P V, once the values have landed; behind the job's last key they become zeros
+        const int t = tile_of(x), j = step_of(x - 2), g = gbase + j;
+        if (!both || t == 0) {
+          if (!(ok = warp_wait(&sm.bar_vfull[g & 1], g >> 1, abort))) break;
+          if (j == nk - 1 && tail < kTile) zero_tail(dev::smem_u32(sm.w.v[g & 1]), tail);
+        }
+        if (!(ok = warp_wait(&sm.bar_p[t], t ? ptot1 : ptot0, abort))) break;
+        if (t) ++ptot1;
+        else ++ptot0;
+        dev::tc_fence_after();
+        if (lane == 0) {
+          const uint64_t b0 = dv0 + static_cast<uint64_t>((g & 1) * kBufStep);
+          const bool acc = both ? j > 0 : j > 1;
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            dev::umma_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, b0 + ((ks * 2 * kGroupBytes) >> 4), idesc_o,
+                         (acc || ks > 0) ? 1u : 0u);
+          if (!both || t == 1) dev::umma_commit(dev::smem_u32(&sm.bar_vempty[g & 1]));
+          if (x >= items) dev::umma_commit(dev::smem_u32(&sm.bar_o[t]));  // the row tile's last
+        }
+        __syncwarp();
       }
-    } else {
-      ok = ok && issue_s(flip, 0, true) && (nk < 2 || issue_s(flip ^ 1, 1, true));
-      for (int j = 0; ok && j < nk; ++j) {
-        const int t = (j & 1) ^ flip;
-        ok = wait_v(j) && issue_pv(t, j, j > 1, true, j + 2 >= nk) && (j + 2 >= nk || issue_s(t, j + 2, true));
+      if (x < items) {
+        const int t = tile_of(x), g = gbase + step_of(x);
+        if (!(ok = warp_wait(&sm.bar_kfull[g & 1], g >> 1, abort))) break;
+        dev::tc_fence_after();
+        if (lane == 0) {
+          const uint64_t a0 = dq0 + static_cast<uint64_t>(both ? t * kBufStep : 0);
+          const uint64_t b0 = dk0 + static_cast<uint64_t>((g & 1) * kBufStep);
+#pragma unroll
+          for (int ks = 0; ks < kD / 16; ++ks) {
+            const uint32_t qoff = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
+            const uint32_t koff = ((ks >> 2) * kGroupHalf + (ks & 3) * 32) >> 4;
+            dev::umma_ss(tmem + t * 128, a0 + qoff, b0 + koff, idesc_s, ks > 0 ? 1u : 0u);
+          }
+          dev::umma_commit(dev::smem_u32(&sm.bar_s[t]));
+          if (x == items - 1) dev::umma_commit(dev::smem_u32(&sm.bar_qempty));
+          if (!both || t == 1) dev::umma_commit(dev::smem_u32(&sm.bar_kempty[g & 1]));
+        }
+        __syncwarp();
       }
     }
     gbase += nk;
@@ -776,42 +764,17 @@ __device__ __forceinline__ void thin_mma(const Cta& ct) {
   constexpr uint32_t idesc_s = dev::idesc_bf16_f32(kTile, kThinRows, 0, 0);  // K tile, Q: K-major
   constexpr uint32_t idesc_o = dev::idesc_bf16_f32(kD, kThinRows, 1, 0);     // V^T MN-major, P^T K-major
   bool ok = true;
-  int taken = 0, used = 0;     // chunks read, tiles taken from the ring
-  int v_nt = 0, v_keys = 0;    // the chunk whose P V is next
-  auto pv = [&](int c) {       // of chunk number c
-    const int g = c & 1;
-    if (!warp_wait(&sm.bar_p[g], c >> 1, abort)) return false;
-    for (int t = 0; t < v_nt; ++t) {
-      const int s = used % kThinStages;
-      if (!warp_wait(&sm.bar_full[s], used / kThinStages, abort)) return false;
-      const uint32_t tile = dev::smem_u32(sm.t.tile[s]);
-      const int tail = v_keys - t * kTile;
-      if (tail < kTile) zero_tail(tile, tail);
-      dev::tc_fence_after();
-      if (lane == 0) {
-        const uint64_t a0 = dev::smem_desc(tile, kGroupHalf, kGroupBytes, dev::kSwizzle128B);
-        const uint64_t b0 = dev::smem_desc(dev::smem_u32(sm.t.p[g][t]), 16, 1024, dev::kSwizzle128B);
-#pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks)
-          dev::umma_ss(ct.tmem + 256 + g * kThinRows, a0 + ((ks * 2 * kGroupBytes) >> 4),
-                       b0 + (((ks >> 2) * kPBlockBytes + (ks & 3) * 32) >> 4), idesc_o, (t > 0 || ks > 0) ? 1u : 0u);
-        dev::umma_commit(dev::smem_u32(&sm.bar_empty[s]));
-        if (t == v_nt - 1) dev::umma_commit(dev::smem_u32(&sm.bar_o[g]));
-      }
-      __syncwarp();
-      ++used;
-    }
-    return true;
-  };
-  while (ok) {
-    const int slot = taken % kChunkSlots;
-    if (!(ok = warp_wait(&sm.bar_chunk_full[slot], taken / kChunkSlots, abort))) break;
-    const int valid = sm.chunk[slot].valid, nt = sm.chunk[slot].nt, keys = sm.chunk[slot].keys;
-    if (!valid) break;
+  int used = 0;              // tiles taken from the ring
+  int v_nt = 0, v_keys = 0;  // of the chunk whose P V is next
+#pragma unroll 1
+  for (int c = 0;; ++c) {    // chunk c, then P V of the chunk before
+    const int slot = c % kChunkSlots, g = c & 1;
+    if (!(ok = warp_wait(&sm.bar_chunk_full[slot], c / kChunkSlots, abort))) break;
+    const int valid = sm.chunk[slot].valid, nt = valid ? sm.chunk[slot].nt : 0, keys = sm.chunk[slot].keys;
     __syncwarp();
-    if (lane == 0) dev::mbar_arrive(dev::smem_u32(&sm.bar_chunk_empty[slot]));
+    if (valid && lane == 0) dev::mbar_arrive(dev::smem_u32(&sm.bar_chunk_empty[slot]));
     // S of this chunk: its columns of tensor memory were read before the P V of the chunk before last
-    const int g = taken & 1;
+#pragma unroll 1
     for (int t = 0; t < nt; ++t) {
       const int s = used % kThinStages;
       if (!(ok = warp_wait(&sm.bar_full[s], used / kThinStages, abort))) break;
@@ -829,12 +792,37 @@ __device__ __forceinline__ void thin_mma(const Cta& ct) {
       __syncwarp();
       ++used;
     }
-    if (ok && taken > 0) ok = pv(taken - 1);
+    if (!ok) break;
+    if (c > 0) {
+      const int pg = g ^ 1;
+      if (!(ok = warp_wait(&sm.bar_p[pg], (c - 1) >> 1, abort))) break;
+#pragma unroll 1
+      for (int t = 0; t < v_nt; ++t) {
+        const int s = used % kThinStages;
+        if (!(ok = warp_wait(&sm.bar_full[s], used / kThinStages, abort))) break;
+        const uint32_t tile = dev::smem_u32(sm.t.tile[s]);
+        const int tail = v_keys - t * kTile;
+        if (tail < kTile) zero_tail(tile, tail);
+        dev::tc_fence_after();
+        if (lane == 0) {
+          const uint64_t a0 = dev::smem_desc(tile, kGroupHalf, kGroupBytes, dev::kSwizzle128B);
+          const uint64_t b0 = dev::smem_desc(dev::smem_u32(sm.t.p[pg][t]), 16, 1024, dev::kSwizzle128B);
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            dev::umma_ss(ct.tmem + 256 + pg * kThinRows, a0 + ((ks * 2 * kGroupBytes) >> 4),
+                         b0 + (((ks >> 2) * kPBlockBytes + (ks & 3) * 32) >> 4), idesc_o, (t > 0 || ks > 0) ? 1u : 0u);
+          dev::umma_commit(dev::smem_u32(&sm.bar_empty[s]));
+          if (t == v_nt - 1) dev::umma_commit(dev::smem_u32(&sm.bar_o[pg]));
+        }
+        __syncwarp();
+        ++used;
+      }
+      if (!ok) break;
+    }
+    if (!valid) break;
     v_nt = nt;
     v_keys = keys;
-    ++taken;
   }
-  if (ok && taken > 0) pv(taken - 1);
   __syncwarp();
   if (lane == 0) {
     dev::umma_commit(dev::smem_u32(&sm.bar_drain));
@@ -913,9 +901,8 @@ __device__ __forceinline__ bool thin_chunk(const Params& p, const Cta& ct, ThinS
   for (int e = 0; e < N; ++e) mx[e] = neg_inf();
   if (ok) {
     dev::tc_fence_after();
-#pragma unroll
-    for (int t = 0; t < kChunk; ++t) {
-      if (t >= nt) break;
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
       uint32_t raw[N];
       ld_cols<N>(ct.tmem + lane_off + (g * kChunk + t) * kThinRows, raw);
       dev::tmem_wait_ld_regs(raw);
@@ -947,9 +934,8 @@ __device__ __forceinline__ bool thin_chunk(const Params& p, const Cta& ct, ThinS
     // that are not real hold anything: they reach only their own columns of O^T.
     const uint32_t kk = static_cast<uint32_t>(i & 63);
     uint8_t* blk = &sm.t.p[g][0][0] + (i >> 6) * kPBlockBytes + (kk & 7) * 2;
-#pragma unroll
-    for (int t = 0; t < kChunk; ++t) {
-      if (t >= nt) break;
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
       uint32_t raw[N];
       ld_cols<N>(ct.tmem + lane_off + (g * kChunk + t) * kThinRows, raw);
       dev::tmem_wait_ld_regs(raw);
@@ -1148,6 +1134,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // shorter than a step
   const int share_wide = max(wide > 0 ? split(cost_wide, wide) : 0, kCostBoth);
   const int share_thin = max(wide < ctas ? split(cost_thin, ctas - wide) : 0, p.thin_cost);
+  // The CTAs of a line stand together: neighbouring SMs share an instruction cache, which holds the code of one
+  // kind, not of both.  (In turn over the grid, a wide step took 5400 clocks instead of 4000 and a thin
+  // one 3500 instead of 2700, with five times the misses.  For the same reason the loops around the
+  // products and over a chunk's tiles are not unrolled: 54 -> 49 us on 97 sequences in 5 groups.)
   const bool is_wide = static_cast<int>(blockIdx.x) < wide;
   Cta ct;
   ct.sm = &sm;
