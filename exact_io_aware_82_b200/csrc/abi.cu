@@ -1240,6 +1240,8 @@ int pfx_shapes(int B, int Hq, int Hkv, int num_groups, int max_prefix_len, int m
     return ATTN_ERR_INVALID_ARG;
   const int G = Hq / Hkv;
   if (d != pfx::kD || (G != 1 && G != 2 && G != 4 && G != 8)) return ATTN_ERR_UNSUPPORTED;
+  // the kernels look up to two tiles past a length
+  if (max_prefix_len > 0x7fffffff - 512 || max_seq_len > 0x7fffffff - 512) return ATTN_ERR_UNSUPPORTED;
   const double blocks = std::min<double>(B, B / (256 / G) + static_cast<double>(num_groups));
   const double cost = Hkv * (blocks * ((max_prefix_len / 128 + 1.0) * pfx::kCostBoth + pfx::kCostWideJob) +
                              static_cast<double>(B) * ((max_seq_len / 128 + 1.0) * pfx::kCostThinMax + pfx::kCostThinJob));

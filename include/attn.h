@@ -358,7 +358,7 @@ ATTN_API int attn_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_
  *             A token with a negative slot is left out (nothing of it is written, q_out included): the
  *             padding of a fixed token count.  A slot past the cache is not followed
  *             either, and the device flag records ATTN_ERR_INVALID_ARG.  Slots of one call are
- *             distinct; of two tokens with one slot, which one the row ends with is not specified.
+ *             distinct; what a row that two tokens name ends with is not specified.
  *   strides   HOST long long [13]: (unused, h, t) of q, k, v, q_out, then the axis stride of positions.
  * Other arguments and rules as attn_qk_norm_rope; rows of the cache that no slot names stay as they are.
  */
@@ -423,10 +423,11 @@ ATTN_API int attn_page_update(int *block_table, const int *old_lens, const int *
  *   prefix's) last key is not used, infinities and NaN included.
  *   workspace    device scratch of at least attn_decode_shared_prefix_workspace_bytes(...) bytes,
  *                16-byte aligned, overwritten before it is read.
- * G = Hq / Hkv in {1, 2, 4, 8}, d == 128, B <= 65535, and steps and partial rows that 32 bits count
- * (ATTN_ERR_UNSUPPORTED otherwise; the workspace size is 0 for arguments that the call refuses).
- * Errors, and page numbers outside the cache, as attn_decode_paged.  The result does not depend on scheduling (no atomics, no counter: captured
- * graphs with workspaces of their own may run at the same time).
+ * G = Hq / Hkv in {1, 2, 4, 8}, d == 128, B <= 65535, and lengths, steps and partial rows that 32 bits
+ * count (ATTN_ERR_UNSUPPORTED otherwise; the workspace size is 0 for sizes that the call refuses).
+ * Errors, and page numbers outside the cache, as attn_decode_paged.  The result does not depend on
+ * scheduling (no atomics, no counter: captured graphs with workspaces of their own may run at the
+ * same time).
  */
 ATTN_API size_t attn_decode_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int num_groups,
                                                           int max_prefix_len, int max_seq_len, int d);

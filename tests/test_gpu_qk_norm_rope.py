@@ -181,6 +181,20 @@ def test_in_place_equals_out_of_place():
     assert torch.equal(zq, q) and torch.equal(zk, k)
 
 
+def test_gradient_in_the_place_of_its_inputs():
+    g = gen(61)
+    q, k = fused(g, 2, 131, 8, 2, 128, BF)
+    wq, wk = weight(g, 128, BF), weight(g, 128, BF)
+    rope = R.rope_table(200, 128).cuda()
+    pos = torch.arange(131, dtype=torch.int32).cuda()
+    dzq, dzk = (normal(g, *x.shape, dtype=BF) for x in (q, k))
+    want = A.attn_qk_norm_rope_bwd(q, k, dzq, dzk, wq, wk, rope, pos)
+    got = A.attn_qk_norm_rope_bwd(q, k, dzq, dzk, wq, wk, rope, pos, dq=q, dk=k)
+    assert got[0] is q and got[1] is k
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
 def test_broadcast_heads_and_positions():
     # one key row shared by all heads (stride 0), positions of one sequence shared by the batch
     g = gen(7)

@@ -117,6 +117,16 @@ def test_shared_prefix_refusals(lib):
     assert need(64, 32, 8, 3, 5000, 100, 128) == -(-rows * 516 // 16) * 16 + 4 * (4 + 2 * 3 + 64)
 
 
+def test_shared_prefix_longest_lengths(lib):
+    # up to two tiles past a length are still counted in 32 bits
+    need = A.attn_decode_shared_prefix_workspace_bytes
+    most = 2 ** 31 - 1 - 512
+    for args in ((most + 1, 0), (0, most + 1), (2 ** 31 - 1, 2 ** 31 - 1)):
+        assert need(1, 1, 1, 1, *args, 128) == 0
+        assert prefix(lib, B_=1, Hq=1, Hkv=1, mpl=args[0], ml=args[1], mp=1 << 30, mpp=1 << 30) == U
+    assert need(1, 1, 1, 1, most, 0, 128) > 0 and need(1, 1, 1, 1, 0, most, 128) > 0
+
+
 def t(*shape, dtype=bf16, device="cpu"):
     return torch.zeros(shape, dtype=dtype, device=device)
 
