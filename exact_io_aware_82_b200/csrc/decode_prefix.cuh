@@ -27,6 +27,10 @@
 // starts: there is no counter and no order of arrival, results are the same in every run, and
 // launches share nothing but the caller's workspace.
 //
+// Measured on a B200 (Hq 32, Hkv 8; both kernels): 64 sequences behind 32768 keys, 400 own at most, 16-key
+// pages: 71.7 us; 256 sequences behind 16384 keys, 1500 own at most, 32-key pages: 201.5 us; 4 behind
+// 700 keys: 15.8 us.  Thin steps alone (64 x 4096 keys): 5.7 TB/s with 16-key pages, 6.2 with 64.
+//
 // Warps (12): 0-3 and 4-7 softmax and epilogue (wide: of row tile 0 and 1, thread = row = TMEM lane;
 // thin: of even and odd chunks of 4 tiles, thread = key, then output column), 8 the tcgen05.mma
 // issuer (all lanes first zero the value rows past a job's last key: what a page holds there may

@@ -22,6 +22,9 @@
 //   - the row sums of an item are reduced together (each step of the exchange halves the values a
 //     lane still carries), so r is computed once per row instead of once per lane and row;
 //   - arithmetic is in pairs of fp32 values.
+// Measured on a B200 (copy rate 6.54 TB/s), bf16, heads of 128: 16384 tokens of 32 + 8 heads 54.8 us, 6.1
+// TB/s; the gradient of 8192 tokens of 16 + 16 heads 41.3 us, 4.9 TB/s (36.8 us without the weights' sum);
+// 16384 tokens into a paged cache 66.6 us, 6.1 TB/s, and 64 tokens 3.2 us.
 #pragma once
 
 #include <cuda.h>
@@ -447,7 +450,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_paged_kernel(c
 // leaves from the same buffer by one TMA store.  The tensor maps carry all strides (those of a fused
 // projection, of head-major or token-major outputs, 0 for broadcast heads), and clip heads and
 // tokens past the last.  So a thread holds no addresses and fits 72 registers: 28 warps per SM with
-// two tiles a block on their way.  A block's tiles all have the same heads.
+// two tiles a block on their way.  (Rows by ordinary loads with the next ones in registers: 65 us
+// instead of 54.8, the moves wait for the loads; a fourth stage, which costs a block per SM: 57.3.)
+// A block's tiles all have the same heads.
 constexpr int kTokens = 4;
 constexpr int kTileThreads = 32 * kTokens;
 constexpr int kTileBlocks = 7;     // per SM: 72 registers a thread
