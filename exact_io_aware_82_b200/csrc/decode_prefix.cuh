@@ -28,8 +28,8 @@
 // launches share nothing but the caller's workspace.
 //
 // Measured on a B200 (Hq 32, Hkv 8; both kernels): 64 sequences behind 32768 keys, 400 own at most, 16-key
-// pages: 71.7 us; 256 sequences behind 16384 keys, 1500 own at most, 32-key pages: 201.5 us; 4 behind
-// 700 keys: 15.8 us.  Thin steps alone (64 x 4096 keys): 5.7 TB/s with 16-key pages, 6.2 with 64.
+// pages: 72.2 us; 256 sequences behind 16384 keys, 1500 own at most, 32-key pages: 200.8 us; 4 behind
+// 700 keys: 15.8 us.  Thin steps alone (64 x 4096 keys): 5.8 TB/s with 16-key pages, 6.4 with 64.
 //
 // Warps (12): 0-3 and 4-7 softmax and epilogue (wide: of row tile 0 and 1, thread = row = TMEM lane;
 // thin: of even and odd chunks of 4 tiles, thread = key, then output column), 8 the tcgen05.mma
@@ -225,12 +225,27 @@ struct Cta {
   int lo, hi;  // its share of the line
 };
 
+// A sequence's own keys are read once and leave L2 first (64 sequences of 4096 keys: 5.74 -> 5.84 TB/s with 16-key
+// pages, 6.16 -> 6.36 with 64; 97 sequences in 5 groups 48.5 -> 47.1 us; to hold a prefix's keys back from
+// leaving, beyond that, changes nothing).
+__device__ __forceinline__ uint64_t prefix_policy() {
+  uint64_t x;
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(x));
+  return x;
+}
+__device__ __forceinline__ uint64_t own_policy() {
+  uint64_t x;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(x));
+  return x;
+}
+
 // One box: `piece` rows of one kv head, both column halves; row0 is a multiple of 8.
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row0, int hk) {
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row0, int hk,
+                                         uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row0 >> 3), "r"(hk)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %3, %3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row0 >> 3), "r"(hk), "l"(policy)
       : "memory");
 }
 
@@ -261,8 +276,9 @@ struct Pieces {
   __device__ __forceinline__ uint32_t bytes(int key0, int len) const {
     return static_cast<uint32_t>(min(pieces, (len - key0 + piece - 1) / piece)) * piece * 256u;
   }
-  __device__ __forceinline__ void load(const CUtensorMap* map, uint32_t dst, uint32_t bar, int page, int row, int hk) const {
-    if (page != -2) load_box(dst + mine * piece * 256, map, bar, row, hk);
+  __device__ __forceinline__ void load(const CUtensorMap* map, uint32_t dst, uint32_t bar, int page, int row, int hk,
+                                       uint64_t policy) const {
+    if (page != -2) load_box(dst + mine * piece * 256, map, bar, row, hk, policy);
   }
 };
 
@@ -291,6 +307,7 @@ __device__ __forceinline__ void wide_produce(const CUtensorMap& tm_q, const CUte
   const int lane = threadIdx.x & 31;
   volatile int* abort = &sm.abort;
   const Pieces pc(p);
+  const uint64_t policy = prefix_policy();
   int published = 0, q_loads = 0, k_issued = 0, v_issued = 0;
   bool ok = true;
 
@@ -328,7 +345,7 @@ __device__ __forceinline__ void wide_produce(const CUtensorMap& tm_q, const CUte
       const uint32_t bar = dev::smem_u32(keys ? &sm.bar_kfull[s] : &sm.bar_vfull[s]);
       if (lane == 0) dev::mbar_arrive_expect_tx(bar, pc.bytes(at, len));
       __syncwarp();
-      pc.load(keys ? &tm_k : &tm_v, dev::smem_u32(keys ? sm.w.k[s] : sm.w.v[s]), bar, page, row, u.hk);
+      pc.load(keys ? &tm_k : &tm_v, dev::smem_u32(keys ? sm.w.k[s] : sm.w.v[s]), bar, page, row, u.hk, policy);
       ++count;
       return true;
     };
@@ -649,6 +666,7 @@ __device__ __forceinline__ void thin_produce(const CUtensorMap& tm_q_thin, const
   struct Source {  // where a chunk's keys are
     const int* table;
     int pages, key0, len, nt, hk;
+    uint64_t policy;
   };
   auto stream = [&](const Source& c, bool keys, const CUtensorMap* map_q, int b0, int cols) {
     int page = pc.page(p, c.table, c.pages, c.key0, c.len);
@@ -666,7 +684,7 @@ __device__ __forceinline__ void thin_produce(const CUtensorMap& tm_q_thin, const
             dev::tma_load_3d(dev::smem_u32(sm.t.q[s]) + half * kQHalfBytes, map_q, bar, half * 64, c.hk * p.G, b0);
       }
       __syncwarp();
-      pc.load(keys ? &tm_k : &tm_v, dev::smem_u32(sm.t.tile[s]), bar, cur, row, c.hk);
+      pc.load(keys ? &tm_k : &tm_v, dev::smem_u32(sm.t.tile[s]), bar, cur, row, c.hk, c.policy);
       ++issued;
     }
   };
@@ -674,7 +692,7 @@ __device__ __forceinline__ void thin_produce(const CUtensorMap& tm_q_thin, const
   before.nt = 0;
   // a run of steps [k0, k1) of one job, as chunks; box: rows of the query box, cols: real ones
   auto run = [&](const int* table, int pages, int len, int hk, int b0, int k0, int k1, const CUtensorMap* map_q,
-                 int box, int cols, long long out) {
+                 int box, int cols, long long out, uint64_t policy) {
     const int chunks = (k1 - k0 + kChunk - 1) / kChunk;
     for (int i = 0; i < chunks; ++i) {
       const int slot = published % kChunkSlots;
@@ -682,7 +700,7 @@ __device__ __forceinline__ void thin_produce(const CUtensorMap& tm_q_thin, const
           !(ok = warp_wait(&sm.bar_chunk_empty[slot], published / kChunkSlots - 1, abort)))
         return;
       Source c;
-      c.table = table, c.pages = pages, c.len = len, c.hk = hk;
+      c.table = table, c.pages = pages, c.len = len, c.hk = hk, c.policy = policy;
       c.key0 = (k0 + i * kChunk) * kTile;
       c.nt = min(kChunk, k1 - k0 - i * kChunk);
       if (lane == 0) {
@@ -721,7 +739,7 @@ __device__ __forceinline__ void thin_produce(const CUtensorMap& tm_q_thin, const
         run(p.prefix_table + static_cast<size_t>(idx) * p.max_prefix_pages, p.max_prefix_pages, g.len, hk, b0, k0,
             k1, &tm_q_thin, thin_seqs * p.G, g.rest * p.G,
             p.thin_row0 + 2ll * p.G * p.Hkv * b0 + 2ll * p.G * g.rest * hk +
-                static_cast<long long>(ct.index) * kThinCtaRows);
+                static_cast<long long>(ct.index) * kThinCtaRows, prefix_policy());
       }
     }
     if (ok && c < ct.hi) {
@@ -737,7 +755,7 @@ __device__ __forceinline__ void thin_produce(const CUtensorMap& tm_q_thin, const
         const int k0 = step_at(ct.lo, c, p.thin_cost), k1 = min(tiles, step_at(ct.hi, c, p.thin_cost));
         if (k0 >= k1) continue;
         run(p.block_table + static_cast<size_t>(idx) * p.max_pages, p.max_pages, len, hk, idx, k0, k1, &tm_q_own,
-            p.G, p.G, p.own_row0 + 2ll * p.G * (static_cast<long long>(idx) * p.Hkv + hk + ct.index));
+            p.G, p.G, p.own_row0 + 2ll * p.G * (static_cast<long long>(idx) * p.Hkv + hk + ct.index), own_policy());
       }
     }
   }
@@ -1141,7 +1159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The CTAs of a line stand together: neighbouring SMs share an instruction cache, which holds the code of one
   // kind, not of both.  (In turn over the grid, a wide step took 5400 clocks instead of 4000 and a thin
   // one 3500 instead of 2700, with five times the misses.  For the same reason the loops around the
-  // products and over a chunk's tiles are not unrolled: 54 -> 49 us on 97 sequences in 5 groups.)
+  // products and over a chunk's tiles are not unrolled: 54 -> 49 us on 97 sequences in 5 groups then.)
   const bool is_wide = static_cast<int>(blockIdx.x) < wide;
   Cta ct;
   ct.sm = &sm;
