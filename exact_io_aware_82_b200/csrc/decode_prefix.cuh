@@ -1251,8 +1251,10 @@ struct Parts {
   int in, rows;   // the first query row within the part; wide: rows of the part, thin: 0
 };
 
+// 64 registers, so that an SM holds the 32 warps that the number of sets counts on (97 sequences of 4 kv heads
+// 46.7 -> 45.4 us); with fewer query heads that spills, and costs 4% on 23 sequences of one kv head.
 template <int G, int kSplit>
-__global__ void __launch_bounds__(32 * G * kSplit)
+__global__ void __launch_bounds__(32 * G * kSplit, G >= 4 ? 32 / (G * kSplit) : 1)
     decode_prefix_combine_kernel(const Params p, __nv_bfloat16* __restrict__ o,
                                  float* __restrict__ lse) {
   constexpr int kRound = 32 / G;                  // parts of a round
