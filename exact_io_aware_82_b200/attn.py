@@ -575,10 +575,10 @@ def _new(dev, stream, dtype, *shape):
     that stream's pool: what the current stream freed last may still be in use there."""
     import torch
 
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+    if stream is None:  # (sizes one by one: a tuple takes a microsecond longer)
+        return torch.empty(*shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = torch.empty(*shape, dtype=dtype, device=dev)
     t.record_stream(torch.cuda.current_stream(dev))
     return t
 
@@ -730,19 +730,18 @@ class _QkShapes:
         if not per_row and shape != lead + (N,):
             raise ValueError("positions must have shape %s%s, got %s" % (
                 lead + (N,), " or %s" % (lead + (B, N),) if self.dense else "", tuple(shape)))
-        if N > 1 and positions.stride(-1) != 1:
+        strides = positions.stride()
+        if N > 1 and strides[-1] != 1:
             raise ValueError("positions must be contiguous in its last dimension")
-        self.pos = (positions.stride(0) if lead else 0, positions.stride(-2) if per_row else 0)
+        self.pos = (strides[0] if lead else 0, strides[-2] if per_row else 0)
         self.N, self.Hq, self.Hkv, self.d = N, Hq, Hkv, d
         # what the library is told: sizes, and from the head size on the rest
         self.sizes = (B, N, Hq, Hkv)
         self.rest = (d, rot, max_pos, axes)
 
 
-def _longs(*parts):
-    """A host array of long long."""
-    flat = [x for p in parts for x in p]
-    return struct.pack("%dq" % len(flat), *flat)
+# host arrays of long long: strides of the forward, backward and paged calls
+_STRIDES, _STRIDES_BWD, _STRIDES_PAGED = (struct.Struct("%dq" % n).pack for n in (14, 20, 13))
 
 
 def attn_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, sections=None, interleaved=False,
@@ -772,7 +771,7 @@ def attn_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, sections=None, 
         k_out = _new(dev, stream, s.dtype, *s.k_shape)
     _call(lib().attn_qk_norm_rope, "attn_qk_norm_rope", dev, stream, q.data_ptr(), k.data_ptr(),
           q_out.data_ptr(), k_out.data_ptr(), _at(q_weight), _at(k_weight), rope.data_ptr(),
-          positions.data_ptr(), _longs(_bhn(q), _bhn(k), _bhn(q_out), _bhn(k_out), s.pos), s.sections,
+          positions.data_ptr(), _STRIDES(*_bhn(q), *_bhn(k), *_bhn(q_out), *_bhn(k_out), *s.pos), s.sections,
           s.code, *s.sizes, *s.rest, 1 if interleaved else 0, float(eps))
     return q_out, k_out
 
@@ -822,7 +821,7 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope, positi
     _call(lib().attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd", dev, stream, q.data_ptr(), k.data_ptr(),
           dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _at(q_weight),
           _at(k_weight), _at(dq_weight), _at(dk_weight), rope.data_ptr(), positions.data_ptr(),
-          _longs(_bhn(q), _bhn(k), _bhn(dq_out), _bhn(dk_out), _bhn(dq), _bhn(dk), s.pos),
+          _STRIDES_BWD(*_bhn(q), *_bhn(k), *_bhn(dq_out), *_bhn(dk_out), *_bhn(dq), *_bhn(dk), *s.pos),
           s.sections, s.code, *s.sizes, *s.rest, 1 if interleaved else 0, float(eps),
           workspace.data_ptr(), workspace.numel())
     return dq, dk, dq_weight, dk_weight
@@ -856,7 +855,7 @@ def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, rope, positions, slots,
     _call(lib().attn_qk_norm_rope_paged, "attn_qk_norm_rope_paged", dev, stream, q.data_ptr(), k.data_ptr(),
           v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _at(q_weight),
           _at(k_weight), rope.data_ptr(), positions.data_ptr(), slots.data_ptr(),
-          _longs(_bhn(q), _bhn(k), _bhn(v), _bhn(q_out), s.pos[:1]), s.sections, s.N, s.Hq, s.Hkv,
+          _STRIDES_PAGED(*_bhn(q), *_bhn(k), *_bhn(v), *_bhn(q_out), s.pos[0]), s.sections, s.N, s.Hq, s.Hkv,
           num_pages, page_size, *s.rest, 1 if interleaved else 0, float(eps))
     return q_out
 
