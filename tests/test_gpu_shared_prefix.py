@@ -226,6 +226,19 @@ def test_random_batches(seed):
     check(c, starts, plens, lens, o, lse, some=sorted(set(rng.integers(0, B, 24).tolist() + [0, B - 1])))
 
 
+@pytest.mark.parametrize("B,ng,Hkv,G", [(5, 1000, 2, 4), (900, 1000, 1, 2), (1500, 3, 2, 8)])
+def test_more_groups_or_sequences_than_threads(B, ng, Hkv, G):
+    # several groups (most of them without a sequence) and several sequences to a thread of the walk
+    rng = np.random.default_rng(B)
+    starts = sorted(rng.integers(0, B + 1, ng + 1).tolist())
+    plens = [int(x) for x in rng.choice([0, 1, 40, 200], ng)]
+    lens = [int(x) for x in rng.integers(0, 90, B)]
+    c = case(400 + B, B, Hkv * G, Hkv, starts, plens, lens, 16)
+    o, lse = A.attn_decode_shared_prefix(**c)
+    torch.cuda.synchronize()
+    check(c, starts, plens, lens, o, lse, some=sorted(set(rng.integers(0, B, 40).tolist() + [0, B - 1])))
+
+
 def test_groups_out_of_order_are_flagged_and_no_prefix_counts():
     lens = [5, 60, 7, 300]
     c = case(133, 4, 8, 2, [0, 2, 4], [70, 900], lens, 16)
