@@ -708,8 +708,12 @@ class _QkShapes:
             Hkv = k_shape[1]
             k_want = (N, Hkv, d)
         self.q_shape, self.k_shape = q_shape, k_want
-        _expect_view(q, "q", dtype, q_shape)
-        _expect_view(k, "k", dtype, k_want)
+        qs, ks = q.stride(), k.stride()
+        if qs[-1] != 1 or k.dtype is not dtype or k_shape != k_want or ks[-1] != 1:
+            _expect_view(q, "q", dtype, q_shape)
+            _expect_view(k, "k", dtype, k_want)
+        # (b, h, n) strides
+        self.qk = qs[:3] + ks[:3] if self.dense else (0, qs[1], qs[0], 0, ks[1], ks[0])
         if q_weight is not None:
             _expect(q_weight, "q_weight", dtype, (d,))
         if k_weight is not None:
@@ -771,7 +775,7 @@ def attn_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, sections=None, 
         k_out = _new(dev, stream, s.dtype, *s.k_shape)
     _call(lib().attn_qk_norm_rope, "attn_qk_norm_rope", dev, stream, q.data_ptr(), k.data_ptr(),
           q_out.data_ptr(), k_out.data_ptr(), _at(q_weight), _at(k_weight), rope.data_ptr(),
-          positions.data_ptr(), _STRIDES(*_bhn(q), *_bhn(k), *_bhn(q_out), *_bhn(k_out), *s.pos), s.sections,
+          positions.data_ptr(), _STRIDES(*s.qk, *_bhn(q_out), *_bhn(k_out), *s.pos), s.sections,
           s.code, *s.sizes, *s.rest, 1 if interleaved else 0, float(eps))
     return q_out, k_out
 
@@ -821,7 +825,7 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope, positi
     _call(lib().attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd", dev, stream, q.data_ptr(), k.data_ptr(),
           dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _at(q_weight),
           _at(k_weight), _at(dq_weight), _at(dk_weight), rope.data_ptr(), positions.data_ptr(),
-          _STRIDES_BWD(*_bhn(q), *_bhn(k), *_bhn(dq_out), *_bhn(dk_out), *_bhn(dq), *_bhn(dk), *s.pos),
+          _STRIDES_BWD(*s.qk, *_bhn(dq_out), *_bhn(dk_out), *_bhn(dq), *_bhn(dk), *s.pos),
           s.sections, s.code, *s.sizes, *s.rest, 1 if interleaved else 0, float(eps),
           workspace.data_ptr(), workspace.numel())
     return dq, dk, dq_weight, dk_weight
@@ -855,7 +859,7 @@ def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, rope, positions, slots,
     _call(lib().attn_qk_norm_rope_paged, "attn_qk_norm_rope_paged", dev, stream, q.data_ptr(), k.data_ptr(),
           v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _at(q_weight),
           _at(k_weight), rope.data_ptr(), positions.data_ptr(), slots.data_ptr(),
-          _STRIDES_PAGED(*_bhn(q), *_bhn(k), *_bhn(v), *_bhn(q_out), s.pos[0]), s.sections, s.N, s.Hq, s.Hkv,
+          _STRIDES_PAGED(*s.qk, *_bhn(v), *_bhn(q_out), s.pos[0]), s.sections, s.N, s.Hq, s.Hkv,
           num_pages, page_size, *s.rest, 1 if interleaved else 0, float(eps))
     return q_out
 
