@@ -53,6 +53,12 @@ __device__ __forceinline__ int pages_of(int len, int shift) {
   return static_cast<int>((static_cast<long long>(len) + (1 << shift) - 1) >> shift);
 }
 
+// work(i) for every step-th i below n, from first on.  Counted without a sign: i + step passes 2^31 where n does not.
+template <typename F>
+__device__ __forceinline__ void every(int first, int step, int n, F&& work) {
+  for (unsigned i = first; i < static_cast<unsigned>(n); i += step) work(static_cast<int>(i));
+}
+
 __global__ void __launch_bounds__(kThreads) page_update_kernel(const Params p) {
   extern __shared__ int smem[];
   int* cu = smem;                // [B + 1] first token of each request
@@ -110,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) page_update_kernel(const Params p) {
   if (missing != 0) {
     // all or nothing: the tables, the ring and its ends stay as they were, no token has a slot
     for (int b = gtid; b <= p.B; b += threads) p.cu[b] = 0;
-    for (int t = gtid; t < p.max_tokens; t += threads) p.slots[t] = -1, p.positions[t] = 0;
+    every(gtid, threads, p.max_tokens, [&](int t) { p.slots[t] = -1, p.positions[t] = 0; });
     return;
   }
   {
@@ -155,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) page_update_kernel(const Params p) {
     p.free_pages[ring(tail0, m)] = p.table[static_cast<size_t>(b) * p.max_pages + need + (m - shrink0[b])];
   }
   // tokens: a thread per token
-  for (int t = gtid; t < p.max_tokens; t += threads) {
+  every(gtid, threads, p.max_tokens, [&](int t) {
     int slot = -1, pos = 0;
     if (t < cu[p.B]) {
       const int lo = find(cu, t);
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) page_update_kernel(const Params p) {
     }
     p.slots[t] = slot;
     p.positions[t] = pos;
-  }
+  });
 }
 
 }  // namespace pages
