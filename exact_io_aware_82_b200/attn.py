@@ -557,6 +557,13 @@ def _expect_view(t, name, dtype, shape, written=False):
             end = step * (n - 1) + end
 
 
+def _fit(**sizes):
+    """Sizes that the C ABI takes as 32 bits: ctypes would cut a larger one down without a word."""
+    for n, v in sizes.items():
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise ValueError("%s must fit in 32 bits, got %d" % (n, v))
+
+
 def _one_device(stream, **tensors):
     """The device of all tensors (and of the stream), as _device."""
     index = None
@@ -612,6 +619,8 @@ def _at(t):
 @functools.lru_cache(maxsize=1024)
 def attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len, max_seq_len,
                                               d) -> int:
+    if max(B, Hq, Hkv, num_groups, max_prefix_len, max_seq_len, d) > 0x7fffffff:
+        return 0  # as for every size that the call refuses
     return int(lib().attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len,
                                                                max_seq_len, d))
 
@@ -646,10 +655,12 @@ def attn_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, gr
     _expect_out(o, "o", torch.bfloat16, (B, Hq, 1, d))
     _expect_out(lse, "lse", torch.float32, (B, Hq))
     _check_workspace(workspace, 0)
+    max_prefix_len, max_seq_len = int(max_prefix_len), int(max_seq_len)
+    _fit(max_prefix_len=max_prefix_len, max_seq_len=max_seq_len, max_prefix_pages=prefix_table.shape[1],
+         max_pages_per_seq=block_table.shape[1])
     dev = _one_device(stream, q=q, k_cache=k_cache, v_cache=v_cache, prefix_table=prefix_table,
                       prefix_lens=prefix_lens, group_starts=group_starts, block_table=block_table,
                       seq_lens=seq_lens, o=o, lse=lse, workspace=workspace)
-    max_prefix_len, max_seq_len = int(max_prefix_len), int(max_seq_len)
     if o is None:
         o = _new(dev, stream, torch.bfloat16, B, Hq, 1, d)
     if lse is None and return_lse:
@@ -888,9 +899,10 @@ def attn_page_update(block_table, old_lens, new_lens, free_pages, ring, page_siz
     _expect(new_lens, "new_lens", torch.int32, (B,))
     _check(free_pages, "free_pages", torch.int32, 1)
     _expect(ring, "ring", torch.int64, (3,))
-    max_tokens = int(max_tokens)
+    max_tokens, page_size = int(max_tokens), int(page_size)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
+    _fit(max_tokens=max_tokens, page_size=page_size, max_pages_per_seq=max_pages, num_pages=free_pages.numel())
     _expect_out(pos_offset, "pos_offset", torch.int32, (B,))
     _expect_out(ring_out, "ring_out", torch.int64, (3,))
     _expect_out(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
@@ -910,7 +922,7 @@ def attn_page_update(block_table, old_lens, new_lens, free_pages, ring, page_siz
     _call(lib().attn_page_update, "attn_page_update", dev, stream, block_table.data_ptr(),
           old_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), ring.data_ptr(),
           ring_out.data_ptr(), cu_seqlens.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-          _at(pos_offset), B, max_pages, int(page_size), free_pages.numel(), max_tokens)
+          _at(pos_offset), B, max_pages, page_size, free_pages.numel(), max_tokens)
     return ring_out, cu_seqlens, slots, positions
 
 
