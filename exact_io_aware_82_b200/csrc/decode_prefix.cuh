@@ -114,8 +114,8 @@ struct Params {
 
 // ---- the lines of jobs (shared with the combine kernel) ----
 struct Group {
-  int b0, n, tiles, len;  // first sequence, sequences, key tiles, keys
-  int full, rest;         // blocks of 2 S sequences, sequences of the last, smaller block
+  int b0 = 0, n = 0, tiles = 0, len = 0;  // first sequence, sequences, key tiles, keys
+  int full = 0, rest = 0;                 // blocks of 2 S sequences, sequences of the last, smaller block
 };
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return max(lo, min(x, hi)); }
@@ -1061,7 +1061,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (loads of the first group and of the first sequence before either is used)
   const int len0 = b0 < b1 ? seq_len(p, b0) : 0;
   Group first;
-  first.n = first.tiles = first.full = first.rest = 0;
   if (g0 < g1) first = load_group(p, g0);
   for (int b = b0; b < b1; ++b) {
     const int tiles = tiles_of(b == b0 ? len0 : seq_len(p, b));
@@ -1244,11 +1243,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // where the job's parts come in halves (even and odd steps or chunks; a half that holds nothing has a
 // log-sum-exp of -infinity), else 1.
 struct Parts {
-  int first, ctas, halves;
-  int row;        // the part's first row in CTA 0 of the line
-  int cta_rows;   // rows from one CTA's part to the next one's
-  int half_rows;  // rows from the first half to the second
-  int in, rows;   // the first query row within the part; wide: rows of the part, thin: 0
+  int first = 0, ctas = 0, halves = 1;
+  int row = 0;           // the part's first row in CTA 0 of the line
+  int cta_rows = 0;      // rows from one CTA's part to the next one's
+  int half_rows = 0;     // rows from the first half to the second
+  int in = 0, rows = 0;  // the first query row within the part; wide: rows of the part, thin: 0
 };
 
 // 64 registers, so that an SM holds the 32 warps that the number of sets counts on (97 sequences of 4 kv heads
@@ -1276,7 +1275,6 @@ __global__ void __launch_bounds__(32 * G * kSplit, G >= 4 ? 32 / (G * kSplit) : 
     if (m != 0xffffffffu) break;
   }
   Group gr;
-  gr.tiles = 0;
   if (g >= 0) {
     gr = load_group(p, g);
     if (b >= gr.b0 + gr.n) gr.tiles = 0;
@@ -1291,8 +1289,6 @@ __global__ void __launch_bounds__(32 * G * kSplit, G >= 4 ? 32 / (G * kSplit) : 
   const int pos_prefix = gr.tiles > 0 ? __ldcg(p.plan + 4 + (thin ? p.num_groups : 0) + g) : 0;
   const int pos_own = __ldcg(p.plan + 4 + 2 * p.num_groups + b);
   Parts x0, x1;  // of the prefix job, of the own job
-  x0.ctas = x1.ctas = 0;
-  x0.halves = 1;
   // the CTA that holds position c of a line: a quotient below 149, so one step puts the approximation right
   auto cta_of = [](int c, int share) {
     int q = static_cast<int>(__fdividef(static_cast<float>(c), static_cast<float>(share)));
