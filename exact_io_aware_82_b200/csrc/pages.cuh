@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kThreads) page_update_kernel(const Params p) {
     }
     return lo;
   };
-  // pages taken, then pages returned: a thread per page
+  // pages taken, then pages returned: a thread per page.  (A page taken holds a new token, which checks its number;
+  // one returned is checked here, before it is anybody else's.)
   const int taken = static_cast<int>(all.grow), returned = static_cast<int>(all.shrink);
   for (int m = gtid; m < taken; m += threads) {
     const int b = find(grow0, m), had = pages_of(__ldg(p.old_lens + b), p.page_shift);
@@ -158,7 +159,9 @@ __global__ void __launch_bounds__(kThreads) page_update_kernel(const Params p) {
   }
   for (int m = gtid; m < returned; m += threads) {
     const int b = find(shrink0, m), need = pages_of(__ldg(p.new_lens + b), p.page_shift);
-    p.free_pages[ring(tail0, m)] = p.table[static_cast<size_t>(b) * p.max_pages + need + (m - shrink0[b])];
+    const int page = p.table[static_cast<size_t>(b) * p.max_pages + need + (m - shrink0[b])];
+    if (page < 0 || page >= p.cap) atomicExch(&g_device_error, ATTN_ERR_INVALID_ARG);
+    p.free_pages[ring(tail0, m)] = page;
   }
   // tokens: a thread per token
   every(gtid, threads, p.max_tokens, [&](int t) {

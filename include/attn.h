@@ -397,7 +397,8 @@ ATTN_API int attn_qk_norm_rope_paged(const void *q, const void *k, const void *v
  * a length, the ring or the number of new tokens (more than max_tokens) is not valid it is -1 and
  * the device flag records ATTN_ERR_INVALID_ARG; either way ring_out keeps head and tail, tables and
  * ring stay as they were, cu_seqlens and positions are 0 and slots -1.  A page number outside the
- * pool that a token falls into gives the slot -1 and is flagged.
+ * pool that a token falls into gives the slot -1 and is flagged; one that a request returns is
+ * flagged and goes into the ring as it is.
  */
 ATTN_API int attn_page_update(int *block_table, const int *old_lens, const int *new_lens,
                               int *free_pages, const long long *ring_in, long long *ring_out,

@@ -1,6 +1,5 @@
 """The operators around attention at the ends of what their calls allow."""
 
-import numpy as np
 import pytest
 import torch
 
@@ -46,3 +45,28 @@ def test_page_update_with_the_largest_token_count(free):
     assert slots[:n].tolist() == want_s and positions[:n].tolist() == want_p
     for t, fill in ((slots, -1), (positions, 0)):
         assert all(bool((x == fill).all()) for x in t[n:].split(1 << 28))
+
+
+@pytest.mark.parametrize("bad", [-1, 6, 1 << 30])
+@pytest.mark.parametrize("new", [0, 3])
+def test_a_page_outside_the_pool_is_flagged_when_it_is_returned(bad, new):
+    # request 1 ends or shrinks; its second page has a number that the pool of six does not have
+    table = torch.tensor([[1, 2, -1, -1], [3, bad, -1, -1]], dtype=torch.int32, device="cuda")
+    pool = torch.tensor([0, 4, 5, -7, -7, -7], dtype=torch.int32, device="cuda")
+    ring = torch.tensor([0, 3, 0], device="cuda")
+    out = A.attn_page_update(table, i32(20, 20), i32(20, new), pool, ring, 16, 4)
+    assert A.attn_get_device_error() == A.ATTN_ERR_INVALID_ARG
+    back = [bad] if new else [3, bad]
+    assert out[0].tolist() == [0, 3 + len(back), 0] and pool.tolist() == [0, 4, 5] + back + [-7] * (3 - len(back))
+    # an entry behind the last page that is kept is nobody's: it is not looked at
+    table = torch.tensor([[1, 2, bad, bad], [3, 0, bad, -1]], dtype=torch.int32, device="cuda")
+    A.attn_page_update(table, i32(20, 20), i32(20, new), pool, ring, 16, 4)
+    assert A.attn_get_device_error() == 0
+
+
+def test_a_page_outside_the_pool_is_flagged_when_it_is_taken():
+    table = torch.full((1, 4), -1, dtype=torch.int32, device="cuda")
+    pool, ring = i32(0, 9, 2), torch.tensor([0, 3, 0], device="cuda")
+    out = A.attn_page_update(table, i32(0), i32(17), pool, ring, 16, 20)
+    assert A.attn_get_device_error() == A.ATTN_ERR_INVALID_ARG
+    assert out[2].tolist() == list(range(16)) + [-1] * 4
