@@ -635,6 +635,7 @@ def attn_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, gr
     group_starts[g] .. group_starts[g+1]-1 (int32 [num_groups+1], device); block_table
     [B,max_pages_per_seq] and seq_lens [B] int32 hold each sequence's own keys.  max_prefix_len and
     max_seq_len are ints >= every length.  Returns (o [B,Hq,1,d] bf16, lse [B,Hq] fp32).
+    Row b of q is sequence b's query (attn_qk_norm_rope_paged returns a row per new token: gather first).
     """
     import torch
 

@@ -426,6 +426,10 @@ ATTN_API int attn_page_update(int *block_table, const int *old_lens, const int *
  *                16-byte aligned, overwritten before it is read.
  * G = Hq / Hkv in {1, 2, 4, 8}, d == 128, B <= 65535, and lengths, steps and partial rows that 32 bits
  * count (ATTN_ERR_UNSUPPORTED otherwise; the workspace size is 0 for sizes that the call refuses).
+ * Scores, maxima, sums, LSE and the parts that are joined are fp32; the weights are rounded to bf16 for
+ * the product with V, and O is rounded once.  attn_decode_paged does the same where it uses the tensor
+ * cores (pages of 64 keys or more) and keeps fp32 weights for smaller pages, so on those its O has about
+ * 0.0017 of relative error (its own rounding) and this one's about 0.0023.
  * Errors, and page numbers outside the cache, as attn_decode_paged.  The result does not depend on
  * scheduling (no atomics, no counter: captured graphs with workspaces of their own may run at the
  * same time).
