@@ -557,10 +557,12 @@ def _expect_view(t, name, dtype, shape, written=False):
             end = step * (n - 1) + end
 
 
-def _fit(**sizes):
-    """Sizes that the C ABI takes as 32 bits: ctypes would cut a larger one down without a word."""
+_MOST = 0x7fffffff  # of a size: the C ABI takes 32 bits, and ctypes would cut a larger one down without a word
+
+
+def _refuse_sizes(**sizes):
     for n, v in sizes.items():
-        if not -0x80000000 <= v <= 0x7fffffff:
+        if not -_MOST <= v <= _MOST:
             raise ValueError("%s must fit in 32 bits, got %d" % (n, v))
 
 
@@ -619,7 +621,7 @@ def _at(t):
 @functools.lru_cache(maxsize=1024)
 def attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len, max_seq_len,
                                               d) -> int:
-    if max(B, Hq, Hkv, num_groups, max_prefix_len, max_seq_len, d) > 0x7fffffff:
+    if max(B, Hq, Hkv, num_groups, max_prefix_len, max_seq_len, d) > _MOST:
         return 0  # as for every size that the call refuses
     return int(lib().attn_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, num_groups, max_prefix_len,
                                                                max_seq_len, d))
@@ -657,8 +659,11 @@ def attn_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, gr
     _expect_out(lse, "lse", torch.float32, (B, Hq))
     _check_workspace(workspace, 0)
     max_prefix_len, max_seq_len = int(max_prefix_len), int(max_seq_len)
-    _fit(max_prefix_len=max_prefix_len, max_seq_len=max_seq_len, max_prefix_pages=prefix_table.shape[1],
-         max_pages_per_seq=block_table.shape[1])
+    prefix_pages, seq_pages = prefix_table.shape[1], block_table.shape[1]
+    if not (-_MOST <= max_prefix_len <= _MOST and -_MOST <= max_seq_len <= _MOST and prefix_pages <= _MOST
+            and seq_pages <= _MOST):
+        _refuse_sizes(max_prefix_len=max_prefix_len, max_seq_len=max_seq_len, max_prefix_pages=prefix_pages,
+                      max_pages_per_seq=seq_pages)
     dev = _one_device(stream, q=q, k_cache=k_cache, v_cache=v_cache, prefix_table=prefix_table,
                       prefix_lens=prefix_lens, group_starts=group_starts, block_table=block_table,
                       seq_lens=seq_lens, o=o, lse=lse, workspace=workspace)
@@ -673,8 +678,8 @@ def attn_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, gr
     _call(lib().attn_decode_shared_prefix, "attn_decode_shared_prefix", dev, stream, q.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), _at(lse), prefix_table.data_ptr(),
           prefix_lens.data_ptr(), group_starts.data_ptr(), block_table.data_ptr(),
-          seq_lens.data_ptr(), B, Hq, Hkv, num_groups, num_pages, page_size, prefix_table.shape[1],
-          max_prefix_len, block_table.shape[1], max_seq_len, d,
+          seq_lens.data_ptr(), B, Hq, Hkv, num_groups, num_pages, page_size, prefix_pages,
+          max_prefix_len, seq_pages, max_seq_len, d,
           1.0 / math.sqrt(d) if scale is None else float(scale), workspace.data_ptr(),
           workspace.numel())
     return o, lse
@@ -903,7 +908,9 @@ def attn_page_update(block_table, old_lens, new_lens, free_pages, ring, page_siz
     max_tokens, page_size = int(max_tokens), int(page_size)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    _fit(max_tokens=max_tokens, page_size=page_size, max_pages_per_seq=max_pages, num_pages=free_pages.numel())
+    num_pages = free_pages.shape[0]
+    if not (max_tokens <= _MOST and -_MOST <= page_size <= _MOST and max_pages <= _MOST and num_pages <= _MOST):
+        _refuse_sizes(max_tokens=max_tokens, page_size=page_size, max_pages_per_seq=max_pages, num_pages=num_pages)
     _expect_out(pos_offset, "pos_offset", torch.int32, (B,))
     _expect_out(ring_out, "ring_out", torch.int64, (3,))
     _expect_out(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
@@ -923,7 +930,7 @@ def attn_page_update(block_table, old_lens, new_lens, free_pages, ring, page_siz
     _call(lib().attn_page_update, "attn_page_update", dev, stream, block_table.data_ptr(),
           old_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), ring.data_ptr(),
           ring_out.data_ptr(), cu_seqlens.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-          _at(pos_offset), B, max_pages, page_size, free_pages.numel(), max_tokens)
+          _at(pos_offset), B, max_pages, page_size, num_pages, max_tokens)
     return ring_out, cu_seqlens, slots, positions
 
 
