@@ -777,7 +777,8 @@ def attn_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, sections=None, 
     (the rotated pairs of each position axis) [axes,N] or [axes,B,N] ([axes,T]).  interleaved pairs
     columns (2i, 2i+1) instead of (i, i + rot_dim/2).
 
-    Returns (q_out, k_out), contiguous unless given; an output may be its input.
+    Returns (q_out, k_out), contiguous unless given; an output may be its input (the same view), and must not
+    overlap the inputs otherwise.
     """
     s = _QkShapes(q, k, q_weight, k_weight, rope, positions, sections)
     if q_out is not None:

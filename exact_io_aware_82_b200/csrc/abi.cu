@@ -1505,7 +1505,7 @@ int attn_page_update(int* block_table, const int* old_lens, const int* new_lens,
   p.page_shift = log2_int(page_size);
   p.cap = num_pages;
   p.max_tokens = max_tokens;
-  // a thread per token, and 16 a request for the pages (the device alone knows how many move)
+  // a thread per token, and 32 a request for the pages (the device alone knows how many move)
   const int want = std::max((max_tokens - 1) / pages::kThreads + 1, (B + pages::kWarps - 1) / pages::kWarps);
   const int blocks = std::max(1, std::min(want, info->num_sms));
   const size_t smem = (3 * static_cast<size_t>(B) + 1) * sizeof(int);

@@ -17,15 +17,15 @@
 // 128-key tile of a job.  How a step is computed depends on the query rows of its job:
 //   both  more than 128 rows (at most 256): S = Q K^T with the rows as M, P from tensor memory for
 //         O += P V; two row tiles take every step, so a key tile read once feeds up to 256 rows.
-//         About 4000 SM clocks a step: scores, softmax of 32768 weights and P V follow each other in each
-//         row tile, and the two row tiles overlap only in part.
+//         2.4 us a step with every SM at it (4.0 TB/s of keys and values): scores, softmax of 32768
+//         weights and P V follow each other in each row tile, and the two row tiles overlap only in part.
 //   alt   17 to 128 rows: the same with the two row tiles holding the same rows and taking
 //         alternate steps, so one step's softmax overlaps the next step's products; even and odd
-//         steps end as two parts.  About 2700 clocks a step.
+//         steps end as two parts.  1.55 us a step with every SM at it, 6.2 TB/s.
 //   thin  at most 16 rows (every sequence's own keys among them): S^T = K Q^T with the keys as M and
 //         16 columns, O^T += V^T P^T; a thread holds a key's few scores, so a step costs far
 //         less than its 64 KB take to arrive.
-// The wide steps (both, alt) are bound by computing, the thin ones by HBM, and they run beside
+// The steps of 256 rows are bound by computing, the others by HBM where all SMs take them, and they run beside
 // each other on different SMs: the steps of each kind stand in a line, weighted by what they cost,
 // the CTAs (persistent, one per SM) are divided between the two lines, and every CTA takes an equal
 // length of its line.  Long prefixes are so cut over many CTAs, short sequences taken several to a
@@ -34,8 +34,11 @@
 // launches share nothing but the caller's workspace.
 //
 // Measured on a B200 (Hq 32, Hkv 8; both kernels): 64 sequences behind 32768 keys, 400 own at most, 16-key
-// pages: 72.2 us; 256 sequences behind 16384 keys, 1500 own at most, 32-key pages: 200.8 us; 4 behind
-// 700 keys: 15.8 us.  Thin steps alone (64 x 4096 keys): 5.8 TB/s with 16-key pages, 6.4 with 64.
+// pages: 71.3 us; 256 sequences behind 16384 keys, 1500 own at most, 32-key pages: 201 us (218-228 where calls
+// follow each other for long, under the power cap at 1.75 GHz); 4 behind 700 keys: 15.7 us.  Own keys alone
+// (64 x 4096 keys): 5.9 TB/s with 16-key pages, 6.3 with 64.  What a call takes beside its steps (launch, plan,
+// first loads, epilogues, the joining kernel): 14.3, 16.9 and 18.7 us around a single tile for 16, 128 and 256 rows;
+// 19, 23 and 25 us where every job is cut over many CTAs (64-key pages, a line through 18944 to 75776 keys).
 //
 // Warps (12): 0-3 and 4-7 softmax and epilogue (wide: of row tile 0 and 1, thread = row = TMEM lane;
 // thin: of even and odd chunks of 4 tiles, thread = key, then output column), 8 the tcgen05.mma
@@ -72,7 +75,8 @@ constexpr uint32_t kGroupBytes = 2048, kGroupHalf = 1024;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 // Costs on the lines, in units of about 245 SM clocks: a step of each kind, and what a job adds (its
-// first products and its epilogue, which overlap other jobs' only in part).  A thin step takes what
+// first products and its epilogue, which overlap other jobs' only in part; charged once a job, though each
+// CTA that the job is cut over has its own).  A thin step takes what
 // its 64 KB take through the TMA unit, which depends on the size of the boxes, so of the pages
 // (page_shift 3, 4, 5, 6 and more: 17, 25, 36 and 40 bytes a clock with 80 SMs at it).
 constexpr int kCostBoth = 16;

@@ -24,7 +24,8 @@
 //   - arithmetic is in pairs of fp32 values.
 // Measured on a B200 (copy rate 6.54 TB/s), bf16, heads of 128: 16384 tokens of 32 + 8 heads 54.8 us, 6.1
 // TB/s; the gradient of 8192 tokens of 16 + 16 heads 41.3 us, 4.9 TB/s (36.8 us without the weights' sum);
-// 16384 tokens into a paged cache 66.6 us, 6.1 TB/s, and 64 tokens 3.2 us.
+// 16384 tokens into a paged cache 66.5 us, 6.1 TB/s, and 64 tokens 3.2 us.  (Rates of heads that fill the tiles, 8 or
+// 4 in bf16: the blocks are shared out evenly between groups of heads, whatever a group holds.)
 #pragma once
 
 #include <cuda.h>
@@ -42,7 +43,9 @@ constexpr int kThreads = 256;  // of the paged form
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;     // row loads of a warp's item, forward
 constexpr int kUnrollBwd = 2;  // backward: of x and of dz
-constexpr int kBlocks = 3;     // per SM, paged form: 80 registers a thread
+// per SM, paged form: 80 registers a thread, which partial rotation of halves (20 bytes spilled, 40 with several axes)
+// and side-by-side pairs with several axes (4) do not quite fit
+constexpr int kBlocks = 3;
 constexpr int kMaxAxes = 4;
 
 // Element strides of a packed [N][H][d] view (d contiguous).
@@ -455,8 +458,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_paged_kernel(c
 // A block's tiles all have the same heads.
 constexpr int kTokens = 4;
 constexpr int kTileThreads = 32 * kTokens;
-constexpr int kTileBlocks = 7;     // per SM: 72 registers a thread
-constexpr int kTileBlocksBwd = 5;  // backward: 96 (6 at 80 spill: 2% slower with several axes, else the same)
+constexpr int kTileBlocks = 7;     // per SM: 72 registers a thread (bf16: 4 to 12 bytes spilled in three of the eight forms)
+constexpr int kTileBlocksBwd = 5;  // backward: 96 (8 bytes spilled by partial rotation of halves with several axes, none
+                                   // else; 6 blocks at 80 spill more: 2% slower with several axes, else the same)
 constexpr int kStages = 3;
 constexpr int kWarpBytes = 2048;  // of a stage: a warp's rows (backward: half of them x, half dz)
 constexpr int kStageBytes = kTokens * kWarpBytes;
